@@ -77,6 +77,19 @@ typedef enum { GMM_BF16 = 0, GMM_F32 = 1, GMM_E4M3 = 2 } gmm_dtype;
 
 typedef enum { GMM_OP_FWD = 0, GMM_OP_DLHS = 1, GMM_OP_DRHS = 2, GMM_OP_BWD = 3 } gmm_op;
 
+/* Activations of the fused epilogues (gmm_fwd_act, gmm_act_bwd). */
+typedef enum {
+  GMM_ACT_NONE = 0,
+  GMM_ACT_RELU = 1,
+  GMM_ACT_SILU = 2,      /* z / (1 + exp(-z)) */
+  GMM_ACT_GELU = 3,      /* z Phi(z), with erf */
+  GMM_ACT_GELU_TANH = 4, /* 0.5 z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) */
+  GMM_ACT_SWIGLU = 5     /* silu(gate) * up over the merged columns [gate | up] */
+} gmm_act;
+
+/* Scores of the router (gmm_router_topk). */
+typedef enum { GMM_SCORE_SOFTMAX = 0, GMM_SCORE_SIGMOID = 1 } gmm_score;
+
 /* Device status bits (gmm_read_device_status, `bits_out`). */
 #define GMM_DEV_GROUP_SIZES 1u
 #define GMM_DEV_SCALE 2u
@@ -213,6 +226,108 @@ gmm_status gmm_fwd_keep_lhs(gmm_operand lhs, gmm_operand rhs, int transpose_rhs,
 gmm_status gmm_fwd_swiglu(gmm_operand lhs, gmm_operand rhs, int transpose_rhs, const int32_t *group_sizes,
                           int32_t G, int64_t M, int64_t K, int64_t N, void *out, gmm_dtype out_dtype, void *ws,
                           size_t ws_bytes, void *stream);
+
+/*
+ * Epilogue of gmm_fwd_act.  act: one of gmm_act.  bias: device float [G, N] or
+ * NULL.  residual: device [M, Nout] of residual_dtype (BF16 or F32) or NULL;
+ * it may be the out buffer itself when both have the same type.  preact:
+ * device bf16 [M, N] that receives z for the backward, or NULL.  16-byte
+ * aligned.
+ */
+typedef struct {
+  gmm_act act;
+  const float *bias;
+  const void *residual;
+  gmm_dtype residual_dtype;
+  void *preact;
+} gmm_epilogue;
+
+/*
+ * Forward gmm with bias, activation and residual in its epilogue:
+ *   z[m, :]   = gmm_fwd(lhs, rhs)[m, :] + bias[g(m), :]
+ *   out[m, :] = act(z[m, :]) + residual[m, :]
+ * With G = 1 this is a dense product.  lhs, rhs, rules, layouts, group_sizes
+ * and the workspace (gmm_workspace_bytes(GMM_OP_FWD, M, K, N, G)) are
+ * gmm_fwd's; z, the activation and the sum are fp32, rounded once to out and
+ * (on its own) to preact.  Nout = N, or N / 2 for GMM_ACT_SWIGLU, which takes
+ * the merged gate|up weights of gmm_fwd_swiglu (N % 256 else GMM_ERR_SHAPE)
+ * and a bias over all N columns.  Rows outside every group are 0 in out and
+ * in preact.  The pages have no counterpart; the epilogue is this library's.
+ */
+gmm_status gmm_fwd_act(gmm_operand lhs, gmm_operand rhs, int transpose_rhs, const int32_t *group_sizes, int32_t G,
+                       int64_t M, int64_t K, int64_t N, const gmm_epilogue *epi, void *out, gmm_dtype out_dtype,
+                       void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Gradient of that epilogue.  dout: bf16 [M, Nout]; preact: bf16 [M, N], the
+ * kept z.  dz: bf16 [M, N] = dout * act'(z) (SwiGLU: d gate | d up), the dout
+ * of gmm_dlhs, tgmm_drhs and gmm_backward; it may be the preact buffer itself
+ * (never dout's: SwiGLU writes twice dout's columns).  dbias: device float
+ * [G, N] or NULL: sum of dz over the group's rows in fp32, before dz is
+ * rounded; the order of the sum depends on the sizes only.  Empty groups get
+ * 0, rows outside every group get dz = 0.  The residual's gradient is dout.
+ * M, N, G as for gmm_fwd (N % 256 for SwiGLU).  Workspace:
+ * gmm_act_bwd_workspace_bytes(M, N, G) (0 for invalid sizes).
+ */
+size_t gmm_act_bwd_workspace_bytes(int64_t M, int64_t N, int32_t G);
+gmm_status gmm_act_bwd(const void *dout_bf16, const void *preact_bf16, gmm_act act, const int32_t *group_sizes,
+                       int32_t G, int64_t M, int64_t N, void *dz_bf16, float *dbias, void *ws, size_t ws_bytes,
+                       void *stream);
+
+/*
+ * A whole mixture-of-experts layer for a few tokens (decoding), in one kernel:
+ *   [gate | up] = x[t] @ W1[e],  h = silu(gate) * up,  e = expert_ids[t, j]
+ *   y[t, :] = sum_j weights[t, j] * (h @ W2[e])
+ * x: bf16 [T, K], used in full (not quantized).  expert_ids: device int32
+ * [T, k]; an id outside [0, G) contributes nothing; the same expert may be
+ * named twice.  weights: device float [T, k].  w1: merged gate|up weights
+ * [G, K, 2F] ([G, 2F, K] with transpose_rhs), w2: [G, F, N] ([G, N, F]), both
+ * E4M3 codes with per-channel scales [G, 2F] and [G, N] (gmm_quantize_rhs)
+ * or both bf16 (scale unused); rule GMM_Q_NONE (block-wise scales return
+ * GMM_ERR_UNSUPPORTED).  h is rounded to bf16 between the products; sums are
+ * fp32 in an order that depends on the routing and the number of SMs only.
+ * y: [T, N] of y_dtype (BF16 or F32).  With E4M3 weights a token with a value
+ * that is not finite (or whose h overflows bf16) gets NaN.
+ * K, F, N multiples of 128, F <= 2^19, T * k <= 1024, G <= 1024.  Every
+ * active expert's weights are read once per 32 of its rows (once for T <= 8):
+ * for large T use gmm_fwd_swiglu, gmm_fwd and gmm_combine_rows.  The kernel is
+ * a cooperative launch on every SM of the device.  Workspace:
+ * gmm_moe_few_workspace_bytes (0 for invalid sizes), read and written within
+ * the call; calls that may overlap need workspaces of their own.
+ */
+size_t gmm_moe_few_workspace_bytes(int64_t T, int32_t k, int32_t G, int64_t K, int64_t F, int64_t N,
+                                   gmm_dtype weight_dtype);
+gmm_status gmm_moe_few(const void *x_bf16, const int32_t *expert_ids, const float *weights, int64_t T, int32_t k,
+                       gmm_operand w1, gmm_operand w2, int transpose_rhs, int32_t G, int64_t K, int64_t F, int64_t N,
+                       void *y, gmm_dtype y_dtype, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * The router: k experts of each token and their weights.  logits: [T, E] F32
+ * or BF16.  p = softmax over the row or sigmoid of each logit, in fp32.
+ * The k largest of p + select_bias (device float [E]), or of the logits when
+ * select_bias is NULL, in descending order, ties to the lowest index (keys
+ * compare as exact numbers: fp32 near-ties are decided in fp64); a NaN key
+ * counts as the largest.  An expert whose logit or key is -inf is never
+ * chosen: a token with fewer than k others gets id -1 and weight 0 for the
+ * rest (gmm_moe_few and gmm_combine_rows skip such ids and slots).
+ *   weights[t, j] = scale * p_j, or with normalize scale * p_j / (sum of the
+ *   chosen p), which is finite even where every chosen p underflows.
+ * expert_ids: device int32 [T, k]; weights: device float [T, k].
+ * E <= 1024, k <= 32, k <= E, T <= 2^24; pointers 16-byte aligned.
+ */
+gmm_status gmm_router_topk(const void *logits, gmm_dtype logits_dtype, int64_t T, int32_t E, int32_t k,
+                           gmm_score score, const float *select_bias, int normalize, float scale, int32_t *expert_ids,
+                           float *weights, void *stream);
+
+/*
+ * Gradient of the router's weights with respect to the logits (the choice
+ * itself has none): dweights [T, k] float, logits and expert_ids as in and
+ * from gmm_router_topk, dlogits [T, E] of the logits' type.  An id outside
+ * [0, E) is skipped whatever its dweight; an id named twice counts twice.
+ */
+gmm_status gmm_router_topk_bwd(const float *dweights, const void *logits, gmm_dtype logits_dtype,
+                               const int32_t *expert_ids, int64_t T, int32_t E, int32_t k, gmm_score score,
+                               int normalize, float scale, void *dlogits, void *stream);
 
 /*
  * Forward gmm without a workspace argument, for callers that cannot allocate
@@ -367,6 +482,16 @@ gmm_status gmm_ep_local_order(const int64_t *recv_counts, int32_t P, int32_t El,
  */
 gmm_status gmm_combine_rows(const void *rows_bf16, int64_t nrows, const int32_t *slot, const float *weight, int64_t T,
                             int32_t k, int64_t N, void *y, gmm_dtype y_dtype, void *stream);
+
+/*
+ * gmm_combine_dweight: the gradient of gmm_combine_rows's weights,
+ *   dweight[t, j] = sum_n dy[t, n] * rows[slot[t, j], n]
+ * (fp32; 0 for a slot outside [0, nrows)).  dy: bf16 [T, N]; rows, slot, T, k
+ * and N (a multiple of 8) as for gmm_combine_rows; dweight: device float
+ * [T, k].  16-byte aligned.  T == 0 or k == 0 is a no-op.
+ */
+gmm_status gmm_combine_dweight(const void *dy_bf16, const void *rows_bf16, int64_t nrows, const int32_t *slot,
+                               int64_t T, int32_t k, int64_t N, float *dweight, void *stream);
 
 /*
  * Synchronizes `stream`, then reads the device status word that the last call

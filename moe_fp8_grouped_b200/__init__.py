@@ -7,8 +7,9 @@ The library is loaded on first use and a missing library raises an error:
 there is no CPU fallback.
 """
 from .ops import (  # noqa: F401
-    DType, GmmError, QRule, gmm_backward, gmm_chunk_capacity, gmm_dlhs, gmm_fwd, gmm_fwd_keep_lhs, gmm_fwd_swiglu,
-    gmm_plan, gmm_quantize, gmm_quantize_rhs, gmm_quantize_rhs_blocks, gmm_read_device_status, gmm_selftest_timeout,
+    DType, GmmError, QRule, gmm_act_bwd, gmm_backward, gmm_chunk_capacity, gmm_combine_dweight, gmm_dlhs, gmm_fwd,
+    gmm_fwd_act, gmm_fwd_keep_lhs, gmm_fwd_swiglu, gmm_moe_few, gmm_plan, gmm_quantize, gmm_quantize_rhs,
+    gmm_quantize_rhs_blocks, gmm_read_device_status, gmm_router_topk, gmm_router_topk_bwd, gmm_selftest_timeout,
     gmm_set_tiles, gmm_set_wait_limit_ns, gmm_status_string, gmm_workspace_bytes, last_launch_count, profile_collect,
     profile_enable, tgmm_drhs, workspace,
 )

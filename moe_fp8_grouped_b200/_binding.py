@@ -20,6 +20,8 @@ Q_NONE, Q_STATIC, Q_DYNAMIC = 0, 1, 2
 DT_BF16, DT_F32, DT_E4M3 = 0, 1, 2
 OP_FWD, OP_DLHS, OP_DRHS, OP_BWD = 0, 1, 2, 3
 DEV_GROUP_SIZES, DEV_SCALE, DEV_TIMEOUT = 1, 2, 4
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH, ACT_SWIGLU = 0, 1, 2, 3, 4, 5
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 TILES_AUTO, TILES_ONE_CTA, TILES_CTA_PAIRS, TILES_CTA_PAIRS_NARROW = 0, 1, 2, 3
 
 # every symbol include/gmm_fp8.h declares
@@ -28,12 +30,19 @@ EXPORTS = ["gmm_workspace_bytes", "gmm_chunk_capacity", "gmm_quantize_rhs", "gmm
            "gmm_status_string", "gmm_last_launch_count", "gmm_profile_enable", "gmm_profile_collect",
            "gmm_fwd_noalloc", "gmm_fwd_swiglu", "gmm_quantize_rhs_blocks", "gmm_gather_rows",
            "gmm_combine_rows", "gmm_backward", "gmm_gather_scale_rows", "gmm_fwd_keep_lhs",
-           "gmm_fwd_noalloc_status", "gmm_set_tiles", "gmm_ep_local_order"]
+           "gmm_fwd_noalloc_status", "gmm_set_tiles", "gmm_ep_local_order", "gmm_fwd_act", "gmm_act_bwd",
+           "gmm_act_bwd_workspace_bytes", "gmm_moe_few", "gmm_moe_few_workspace_bytes", "gmm_router_topk",
+           "gmm_router_topk_bwd", "gmm_combine_dweight"]
 
 
 class Operand(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int), ("scale", ctypes.c_void_p),
                 ("rule", ctypes.c_int)]
+
+
+class Epilogue(ctypes.Structure):
+    _fields_ = [("act", ctypes.c_int), ("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p),
+                ("residual_dtype", ctypes.c_int), ("preact", ctypes.c_void_p)]
 
 
 class ProfileEntry(ctypes.Structure):
@@ -81,6 +90,26 @@ def lib():
     L.gmm_ep_local_order.argtypes = [vp, i32, i32, i64, vp, vp, vp, vp]
     L.gmm_ep_local_order.restype = st
     L.gmm_fwd_swiglu.restype = st
+    L.gmm_fwd_act.argtypes = [Operand, Operand, ctypes.c_int, vp, i32, i64, i64, i64, ctypes.POINTER(Epilogue), vp,
+                              ctypes.c_int, vp, sz, vp]
+    L.gmm_fwd_act.restype = st
+    L.gmm_act_bwd_workspace_bytes.argtypes = [i64, i64, i32]
+    L.gmm_act_bwd_workspace_bytes.restype = sz
+    L.gmm_act_bwd.argtypes = [vp, vp, ctypes.c_int, vp, i32, i64, i64, vp, vp, vp, sz, vp]
+    L.gmm_act_bwd.restype = st
+    L.gmm_moe_few_workspace_bytes.argtypes = [i64, i32, i32, i64, i64, i64, ctypes.c_int]
+    L.gmm_moe_few_workspace_bytes.restype = sz
+    L.gmm_moe_few.argtypes = [vp, vp, vp, i64, i32, Operand, Operand, ctypes.c_int, i32, i64, i64, i64, vp,
+                              ctypes.c_int, vp, sz, vp]
+    L.gmm_moe_few.restype = st
+    L.gmm_router_topk.argtypes = [vp, ctypes.c_int, i64, i32, i32, ctypes.c_int, vp, ctypes.c_int, ctypes.c_float, vp,
+                                  vp, vp]
+    L.gmm_router_topk.restype = st
+    L.gmm_router_topk_bwd.argtypes = [vp, vp, ctypes.c_int, vp, i64, i32, i32, ctypes.c_int, ctypes.c_int,
+                                      ctypes.c_float, vp, vp]
+    L.gmm_router_topk_bwd.restype = st
+    L.gmm_combine_dweight.argtypes = [vp, vp, i64, vp, i64, i32, i64, vp, vp]
+    L.gmm_combine_dweight.restype = st
     L.gmm_fwd_noalloc.argtypes = [Operand, Operand, ctypes.c_int, vp, i32, i64, i64, i64, vp, ctypes.c_int, vp]
     L.gmm_fwd_noalloc.restype = st
     L.gmm_fwd_noalloc_status.argtypes = [ctypes.POINTER(ctypes.c_uint32), vp]

@@ -8,7 +8,10 @@
 #include <string>
 #include <vector>
 
+#include "epilogue.h"
+#include "few.h"
 #include "internal.h"
+#include "router.h"
 
 namespace gmm {
 
@@ -371,12 +374,14 @@ gmm_status gmm_quantize(const void *x_bf16, int64_t rows, int64_t cols, gmm_qrul
 
 }  // extern "C"
 
-// Forward pass shared by gmm_fwd (F == 0), gmm_fwd_swiglu (F = N / 2) and
+// Forward pass shared by gmm_fwd (F == 0), gmm_fwd_swiglu (F = N / 2),
 // gmm_fwd_keep_lhs (codes_out != NULL: the lhs codes and dynamic scales are
-// written to the caller's buffers instead of the workspace).
+// written to the caller's buffers instead of the workspace) and gmm_fwd_act
+// (epi != NULL).
 static gmm_status fwd_impl(gmm_operand lhs, gmm_operand rhs, int transpose_rhs, const int32_t *group_sizes, int32_t G,
                            int64_t M, int64_t K, int64_t N, void *out, gmm_dtype out_dtype, void *ws, size_t ws_bytes,
-                           void *stream, int64_t F, uint8_t *codes_out = nullptr, float *scales_out = nullptr) {
+                           void *stream, int64_t F, uint8_t *codes_out = nullptr, float *scales_out = nullptr,
+                           const gmm_epilogue *epi = nullptr) {
   g_launches = 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   gmm_status s = check_sizes(M, K, N, G);
@@ -439,13 +444,20 @@ static gmm_status fwd_impl(gmm_operand lhs, gmm_operand rhs, int transpose_rhs, 
   p.out = out;
   p.out_f32 = out_dtype == GMM_F32;
   p.ld_out = F ? F : N;
+  if (epi) {
+    p.bias = epi->bias;
+    p.residual = epi->residual;
+    p.res_f32 = epi->residual_dtype == GMM_F32;
+    p.preact = epi->preact;
+    p.act = epi->act;
+  }
   p.status = P.status;
   p.wait_limit_ns = g_wait_limit_ns;
   // per-block promotion for dynamic lhs scales or block-wise rhs scales
   const GemmConfig cfg{blk ? MODE_ROWS_BLK : MODE_ROWS, elem, bmn, elem == 1 && (dyn || blk), pairs,
-                       blk ? 256 : tn};
+                       blk ? 256 : tn, epi != nullptr};
   const int grid = row_pass_grid(pairs, M, N, G, cfg.tile_n);
-  if ((s = cuda_status(prof(F ? "gemm_fwd_swiglu" : "gemm_fwd", st,
+  if ((s = cuda_status(prof(epi ? "gemm_fwd_act" : (F ? "gemm_fwd_swiglu" : "gemm_fwd"), st,
                             [&] { return launch_gemm(cfg, tmA, tmB, tmA, p, grid, st); }))) != GMM_OK)
     return s;
   g_launches = n + 1;
@@ -517,7 +529,7 @@ static gmm_status run_dlhs_gemm(const void *A, const float *A_scales, int elem, 
   p.ld_out = K;
   p.status = P.status;
   p.wait_limit_ns = g_wait_limit_ns;
-  const GemmConfig cfg{blk ? MODE_ROWS_BLK : MODE_ROWS, elem, bmn, elem == 1, pairs, tn};
+  const GemmConfig cfg{blk ? MODE_ROWS_BLK : MODE_ROWS, elem, bmn, elem == 1, pairs, tn, false};
   const int grid = row_pass_grid(pairs, M, K, G, tn);
   return cuda_status(prof("gemm_dlhs", st, [&] { return launch_gemm(cfg, tmA, tmB, tmA, p, grid, st); }));
 }
@@ -564,7 +576,7 @@ static gmm_status run_drhs_gemm(int elem, bool dyn, const float *static_scale, i
   p.ld_out = N;
   p.status = P.status;
   p.wait_limit_ns = g_wait_limit_ns;
-  const GemmConfig cfg{MODE_TGMM, elem, false, elem == 1, pairs, tn};
+  const GemmConfig cfg{MODE_TGMM, elem, false, elem == 1, pairs, tn, false};
   const int64_t items = static_cast<int64_t>(G) * (N / (pairs ? 2 * kBlk : kBlk)) * ((K + tn - 1) / tn);
   const int grid = pairs ? static_cast<int>(items < INT_MAX ? items : INT_MAX)
                          : static_cast<int>(items < num_sms() ? items : num_sms());
@@ -716,6 +728,253 @@ gmm_status gmm_backward(gmm_operand lhs, gmm_operand dout, gmm_operand rhs, int 
   g_launches = 5;
   return GMM_OK;
 }
+
+}  // extern "C"
+
+// ------------------------------------------------- fused epilogue, few tokens, router
+
+static bool is_act(int a) { return a >= GMM_ACT_NONE && a <= GMM_ACT_SWIGLU; }
+
+// Workspace of gmm_act_bwd: status header, group plan, column sums per tile.
+struct ActBwdLayout {
+  size_t offs, tpre, partial, total;
+};
+
+static ActBwdLayout act_bwd_layout(int64_t M, int64_t N, int32_t G) {
+  ActBwdLayout L;
+  L.offs = sizeof(WsHeader);
+  L.tpre = L.offs + align256(sizeof(int) * (G + 1));
+  L.partial = L.tpre + align256(sizeof(int) * (G + 1));
+  L.total = L.partial + align256(sizeof(float) * static_cast<size_t>(chunk_capacity(M, G)) * N);
+  return L;
+}
+
+// Workspace of gmm_moe_few: status header, bf16 rows between the products,
+// fp32 partial sums (of either product: the second overwrites the first's).
+struct FewLayout {
+  size_t h, partial, total;
+};
+
+static gmm_status check_few(int64_t T, int32_t k, int32_t G, int64_t K, int64_t F, int64_t N) {
+  if (T <= 0 || k <= 0 || K <= 0 || F <= 0 || N <= 0 || G <= 0) return GMM_ERR_SHAPE;
+  if (K % kBlk || F % kBlk || N % kBlk) return GMM_ERR_SHAPE;
+  if (T > kFewMaxPairs || k > kFewMaxPairs || T * k > kFewMaxPairs) return GMM_ERR_UNSUPPORTED;
+  if (F > (1 << 19)) return GMM_ERR_UNSUPPORTED;
+  const gmm_status s = check_sizes(1, K, 2 * F, G);
+  return s != GMM_OK ? s : check_sizes(1, F, N, G);
+}
+
+static FewLayout few_layout(int64_t T, int32_t k, int64_t K, int64_t F, int64_t N, int elem) {
+  const int64_t pairs = T * k, bke = kBlk / elem;
+  const int64_t p1 = few_parts(2 * F / kBlk, K / bke) * 2 * F, p2 = few_parts(N / kBlk, F / bke) * N;
+  FewLayout L;
+  L.h = sizeof(WsHeader);
+  L.partial = L.h + align256(static_cast<size_t>(pairs) * F * 2);
+  L.total = L.partial + align256(sizeof(float) * static_cast<size_t>(pairs) * (p1 > p2 ? p1 : p2));
+  return L;
+}
+
+extern "C" {
+
+gmm_status gmm_fwd_act(gmm_operand lhs, gmm_operand rhs, int transpose_rhs, const int32_t *group_sizes, int32_t G,
+                       int64_t M, int64_t K, int64_t N, const gmm_epilogue *epi, void *out, gmm_dtype out_dtype,
+                       void *ws, size_t ws_bytes, void *stream) {
+  g_launches = 0;
+  if (!epi || !is_act(epi->act)) return GMM_ERR_INVALID_ARG;
+  if (epi->act == GMM_ACT_SWIGLU && (N <= 0 || N % (2 * kBlk))) return GMM_ERR_SHAPE;
+  if (epi->residual && epi->residual_dtype != GMM_BF16 && epi->residual_dtype != GMM_F32) return GMM_ERR_INVALID_ARG;
+  if ((epi->bias && !al16(epi->bias)) || (epi->residual && !al16(epi->residual)) ||
+      (epi->preact && !al16(epi->preact)))
+    return GMM_ERR_ALIGNMENT;
+  return fwd_impl(lhs, rhs, transpose_rhs, group_sizes, G, M, K, N, out, out_dtype, ws, ws_bytes, stream,
+                  epi->act == GMM_ACT_SWIGLU ? N / 2 : 0, nullptr, nullptr, epi);
+}
+
+size_t gmm_act_bwd_workspace_bytes(int64_t M, int64_t N, int32_t G) {
+  if (check_sizes(M, kBlk, N, G) != GMM_OK) return 0;
+  return act_bwd_layout(M, N, G).total;
+}
+
+gmm_status gmm_act_bwd(const void *dout_bf16, const void *preact_bf16, gmm_act act, const int32_t *group_sizes,
+                       int32_t G, int64_t M, int64_t N, void *dz_bf16, float *dbias, void *ws, size_t ws_bytes,
+                       void *stream) {
+  g_launches = 0;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (!dout_bf16 || !preact_bf16 || !dz_bf16 || !group_sizes || !is_act(act)) return GMM_ERR_INVALID_ARG;
+  gmm_status s = check_sizes(M, kBlk, N, G);
+  if (s != GMM_OK) return s;
+  if (act == GMM_ACT_SWIGLU && N % (2 * kBlk)) return GMM_ERR_SHAPE;
+  if (!al16(dout_bf16) || !al16(preact_bf16) || !al16(dz_bf16) || !al16(ws) || (dbias && !al16(dbias)))
+    return GMM_ERR_ALIGNMENT;
+  const ActBwdLayout L = act_bwd_layout(M, N, G);
+  if (!ws || ws_bytes < (dbias ? L.total : L.partial)) return GMM_ERR_WORKSPACE;
+  uint8_t *w = static_cast<uint8_t *>(ws);
+  ActBwdParams p{};
+  p.dout = static_cast<const __nv_bfloat16 *>(dout_bf16);
+  p.z = static_cast<const __nv_bfloat16 *>(preact_bf16);
+  p.dz = static_cast<__nv_bfloat16 *>(dz_bf16);
+  p.partial = dbias ? reinterpret_cast<float *>(w + L.partial) : nullptr;
+  int *offs = reinterpret_cast<int *>(w + L.offs), *tpre = reinterpret_cast<int *>(w + L.tpre);
+  p.offs = offs;
+  p.tpre = tpre;
+  p.G = G;
+  p.M = M;
+  p.N = N;
+  p.F = act == GMM_ACT_SWIGLU ? N / 2 : N;
+  s = cuda_status(prof("plan", st, [&] {
+    return launch_plan(group_sizes, G, M, offs, tpre, reinterpret_cast<uint32_t *>(w), st);
+  }));
+  if (s != GMM_OK) return s;
+  if ((s = cuda_status(prof("act_bwd", st, [&] { return launch_act_bwd(act, p, st); }))) != GMM_OK) return s;
+  if (dbias &&
+      (s = cuda_status(prof("dbias", st, [&] { return launch_dbias(p.partial, tpre, G, N, dbias, st); }))) != GMM_OK)
+    return s;
+  g_launches = dbias ? 3 : 2;
+  return GMM_OK;
+}
+
+size_t gmm_moe_few_workspace_bytes(int64_t T, int32_t k, int32_t G, int64_t K, int64_t F, int64_t N,
+                                   gmm_dtype weight_dtype) {
+  if (check_few(T, k, G, K, F, N) != GMM_OK || (weight_dtype != GMM_E4M3 && weight_dtype != GMM_BF16)) return 0;
+  return few_layout(T, k, K, F, N, weight_dtype == GMM_E4M3 ? 1 : 2).total;
+}
+
+gmm_status gmm_moe_few(const void *x_bf16, const int32_t *expert_ids, const float *weights, int64_t T, int32_t k,
+                       gmm_operand w1, gmm_operand w2, int transpose_rhs, int32_t G, int64_t K, int64_t F, int64_t N,
+                       void *y, gmm_dtype y_dtype, void *ws, size_t ws_bytes, void *stream) {
+  g_launches = 0;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  gmm_status s = check_few(T, k, G, K, F, N);
+  if (s != GMM_OK) return s;
+  if (!x_bf16 || !expert_ids || !weights || !w1.data || !w2.data || !y) return GMM_ERR_INVALID_ARG;
+  if (y_dtype != GMM_BF16 && y_dtype != GMM_F32) return GMM_ERR_INVALID_ARG;
+  if (w1.dtype != w2.dtype || (w1.dtype != GMM_E4M3 && w1.dtype != GMM_BF16)) return GMM_ERR_INVALID_ARG;
+  const int elem = w1.dtype == GMM_E4M3 ? 1 : 2;
+  if (elem == 1 && (!w1.scale || !w2.scale)) return GMM_ERR_INVALID_ARG;
+  if (w1.rule != GMM_Q_NONE || w2.rule != GMM_Q_NONE) return GMM_ERR_UNSUPPORTED;  // per-channel scales only
+  if (!al16(x_bf16) || !al16(w1.data) || !al16(w2.data) || !al16(y) || !al16(ws) ||
+      (elem == 1 && (!al16(w1.scale) || !al16(w2.scale))))
+    return GMM_ERR_ALIGNMENT;
+  const FewLayout L = few_layout(T, k, K, F, N, elem);
+  if (!ws || ws_bytes < L.total) return GMM_ERR_WORKSPACE;
+  uint8_t *w = static_cast<uint8_t *>(ws);
+  const bool mn = transpose_rhs == 0;
+  const uint32_t bke = kBlk / elem;
+  // boxes: bke columns x bke contraction rows of [G, K, N]; 128 rows of [G, N, K]
+  auto map = [&](CUtensorMap *m, const void *data, int64_t C, int64_t cols) {
+    return mn ? make_map(m, data, elem, cols, static_cast<uint64_t>(G) * C, cols * elem, bke, bke)
+              : make_map(m, data, elem, C, static_cast<uint64_t>(G) * cols, C * elem, bke, kBlk);
+  };
+  CUtensorMap tm1, tm2;
+  if (!map(&tm1, w1.data, K, 2 * F) || !map(&tm2, w2.data, F, N)) return GMM_ERR_CUDA;
+  FewParams p{};
+  p.x = static_cast<const __nv_bfloat16 *>(x_bf16);
+  p.ids = expert_ids;
+  p.weights = weights;
+  p.s1 = elem == 1 ? w1.scale : nullptr;
+  p.s2 = elem == 1 ? w2.scale : nullptr;
+  p.h = reinterpret_cast<__nv_bfloat16 *>(w + L.h);
+  p.partial = reinterpret_cast<float *>(w + L.partial);
+  p.y = y;
+  p.T = static_cast<int>(T);
+  p.k = k;
+  p.pairs = static_cast<int>(T * k);
+  p.G = G;
+  p.F = static_cast<int>(F);
+  p.N = static_cast<int>(N);
+  p.tiles1 = static_cast<int>(2 * F / kBlk);
+  p.kb1 = static_cast<int>(K / bke);
+  p.tiles2 = static_cast<int>(N / kBlk);
+  p.kb2 = static_cast<int>(F / bke);
+  p.y_f32 = y_dtype == GMM_F32;
+  p.status = reinterpret_cast<uint32_t *>(w);
+  p.wait_limit_ns = g_wait_limit_ns;
+  s = cuda_status(prof("moe_few", st, [&] { return launch_moe_few(elem, mn, tm1, tm2, p, st); }));
+  if (s == GMM_OK) g_launches = 1;
+  return s;
+}
+
+static gmm_status check_router(const void *logits, gmm_dtype dtype, int64_t T, int32_t E, int32_t k, gmm_score score) {
+  if (T <= 0 || E <= 0 || k <= 0 || k > E) return GMM_ERR_SHAPE;
+  if (T > (1 << 24) || E > kMaxGroups || k > 32) return GMM_ERR_UNSUPPORTED;
+  if (!logits || (dtype != GMM_F32 && dtype != GMM_BF16)) return GMM_ERR_INVALID_ARG;
+  if (score != GMM_SCORE_SOFTMAX && score != GMM_SCORE_SIGMOID) return GMM_ERR_INVALID_ARG;
+  return GMM_OK;
+}
+
+gmm_status gmm_router_topk(const void *logits, gmm_dtype logits_dtype, int64_t T, int32_t E, int32_t k,
+                           gmm_score score, const float *select_bias, int normalize, float scale, int32_t *expert_ids,
+                           float *weights, void *stream) {
+  g_launches = 0;
+  gmm_status s = check_router(logits, logits_dtype, T, E, k, score);
+  if (s != GMM_OK) return s;
+  if (!expert_ids || !weights) return GMM_ERR_INVALID_ARG;
+  if (!al16(logits) || !al16(expert_ids) || !al16(weights) || (select_bias && !al16(select_bias)))
+    return GMM_ERR_ALIGNMENT;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  RouterParams p{};
+  p.logits = logits;
+  p.bf16 = logits_dtype == GMM_BF16;
+  p.bias = select_bias;
+  p.T = T;
+  p.E = E;
+  p.k = k;
+  p.sigmoid = score == GMM_SCORE_SIGMOID;
+  p.normalize = normalize != 0;
+  p.scale = scale;
+  p.ids = expert_ids;
+  p.weights = weights;
+  s = cuda_status(prof("router_topk", st, [&] { return launch_router_topk(p, st); }));
+  if (s == GMM_OK) g_launches = 1;
+  return s;
+}
+
+gmm_status gmm_router_topk_bwd(const float *dweights, const void *logits, gmm_dtype logits_dtype,
+                               const int32_t *expert_ids, int64_t T, int32_t E, int32_t k, gmm_score score,
+                               int normalize, float scale, void *dlogits, void *stream) {
+  g_launches = 0;
+  gmm_status s = check_router(logits, logits_dtype, T, E, k, score);
+  if (s != GMM_OK) return s;
+  if (!dweights || !expert_ids || !dlogits) return GMM_ERR_INVALID_ARG;
+  if (!al16(logits) || !al16(expert_ids) || !al16(dweights) || !al16(dlogits)) return GMM_ERR_ALIGNMENT;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  RouterParams p{};
+  p.logits = logits;
+  p.bf16 = logits_dtype == GMM_BF16;
+  p.T = T;
+  p.E = E;
+  p.k = k;
+  p.sigmoid = score == GMM_SCORE_SIGMOID;
+  p.normalize = normalize != 0;
+  p.scale = scale;
+  p.ids = const_cast<int32_t *>(expert_ids);
+  p.dweights = dweights;
+  p.dlogits = dlogits;
+  s = cuda_status(prof("router_topk_bwd", st, [&] { return launch_router_topk_bwd(p, st); }));
+  if (s == GMM_OK) g_launches = 1;
+  return s;
+}
+
+gmm_status gmm_combine_dweight(const void *dy_bf16, const void *rows_bf16, int64_t nrows, const int32_t *slot,
+                               int64_t T, int32_t k, int64_t N, float *dweight, void *stream) {
+  g_launches = 0;
+  if (nrows < 0 || T < 0 || k < 0 || N <= 0) return GMM_ERR_INVALID_ARG;
+  if (N % 8) return GMM_ERR_SHAPE;
+  if (T > INT_MAX) return GMM_ERR_UNSUPPORTED;
+  if (T == 0 || k == 0) return GMM_OK;
+  if (!dy_bf16 || (nrows && !rows_bf16) || !slot || !dweight) return GMM_ERR_INVALID_ARG;
+  if (!al16(dy_bf16) || !al16(rows_bf16) || !al16(slot) || !al16(dweight)) return GMM_ERR_ALIGNMENT;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const gmm_status s = cuda_status(prof("combine_dweight", st, [&] {
+    return launch_combine_dweight(dy_bf16, rows_bf16, slot, T, k, nrows, N, dweight, st);
+  }));
+  if (s == GMM_OK) g_launches = 1;
+  return s;
+}
+
+}  // extern "C"
+
+extern "C" {
 
 gmm_status gmm_read_device_status(const void *ws, uint32_t *bits_out, void *stream) {
   if (!ws) return GMM_ERR_INVALID_ARG;

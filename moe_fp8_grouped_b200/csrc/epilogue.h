@@ -1,0 +1,24 @@
+// epilogue.h -- interface between api.cu and the epilogue gradient (epilogue.cu).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace gmm {
+
+struct ActBwdParams {
+  const __nv_bfloat16 *dout;  // [M, F]
+  const __nv_bfloat16 *z;     // [M, N]
+  __nv_bfloat16 *dz;          // [M, N]
+  float *partial;             // [tiles, N] column sums of each 128-row tile, or NULL
+  const int *offs, *tpre;     // group plan
+  int G;
+  int64_t M, N, F;            // N = F, or 2 F for SwiGLU
+};
+
+cudaError_t launch_act_bwd(int act, const ActBwdParams &p, cudaStream_t st);
+cudaError_t launch_dbias(const float *partial, const int *tpre, int G, int64_t N, float *dbias, cudaStream_t st);
+
+}  // namespace gmm

@@ -68,6 +68,7 @@
 // out[M, F]; the 2F-wide product never reaches memory.
 #include <cuda_bf16.h>
 
+#include "epi.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -140,9 +141,6 @@ __device__ __forceinline__ int tile_col_n(int ct, int c, int F) {
   return F ? (c < 128 ? 128 * ct + c : F + 128 * ct + (c - 128)) : kBN * ct + c;
 }
 
-// x * sigmoid(x); -0 for large negative x, where exp(-x) overflows
-__device__ __forceinline__ float silu(float x) { return x / (1.0f + expf(-x)); }
-
 template <int kMode>
 __device__ __forceinline__ Item decode_item(int w, const GemmParams &p, const int *s_offs, const int *s_tpre,
                                             int tn) {
@@ -183,51 +181,6 @@ __device__ __forceinline__ Item decode_item(int w, const GemmParams &p, const in
   return t;
 }
 
-__device__ __forceinline__ void st_v8(void *dst, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t a4,
-                                      uint32_t a5, uint32_t a6, uint32_t a7) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(a0), "r"(a1), "r"(a2),
-               "r"(a3), "r"(a4), "r"(a5), "r"(a6), "r"(a7)
-               : "memory");
-}
-
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-  __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<uint32_t *>(&b);
-}
-
-// Stores 32 consecutive outputs of one row.  v8: the destination is 32-byte
-// aligned, so each instruction writes one full 32-byte sector.
-__device__ __forceinline__ void store_row32(void *out, int64_t off_elems, const float (&v)[32], int out_f32,
-                                            bool v8) {
-  if (out_f32) {
-    float *dst = static_cast<float *>(out) + off_elems;
-    if (v8) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        st_v8(dst + 8 * i, __float_as_uint(v[8 * i]), __float_as_uint(v[8 * i + 1]), __float_as_uint(v[8 * i + 2]),
-              __float_as_uint(v[8 * i + 3]), __float_as_uint(v[8 * i + 4]), __float_as_uint(v[8 * i + 5]),
-              __float_as_uint(v[8 * i + 6]), __float_as_uint(v[8 * i + 7]));
-    } else {
-      float4 *d4 = reinterpret_cast<float4 *>(dst);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) d4[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-    }
-  } else {
-    __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(out) + off_elems;
-    uint32_t w[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-    if (v8) {
-      st_v8(dst, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
-      st_v8(dst + 16, w[8], w[9], w[10], w[11], w[12], w[13], w[14], w[15]);
-    } else {
-      uint4 *d4 = reinterpret_cast<uint4 *>(dst);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) d4[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-    }
-  }
-}
-
 // Stores 32 outputs of one tile row that are one column of the output
 // (dW[g, k0 + j, n] for j < 32, stride `pitch` elements).  The 32 lanes of a
 // warp hold 32 consecutive n, so each instruction writes 128 (f32) or 64
@@ -245,7 +198,7 @@ __device__ __forceinline__ void store_col32(void *out, int64_t off_elems, int64_
   }
 }
 
-template <int kElem, bool kBMN, bool kPromote, int kMode>
+template <int kElem, bool kBMN, bool kPromote, int kMode, bool kEpi>
 __global__ void __launch_bounds__(kThreads, 1)
     gmm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                   const __grid_constant__ CUtensorMap tmOut, const GemmParams p) {
@@ -715,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               const float *fg = cf + colt(c), *fu = cf + colt(c + 2);
-              float o[32];
+              float o[32], ov[kEpi ? 32 : 1];
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
                 const float2 a = acc[c * 16 + i], b2 = acc[(c + 2) * 16 + i];
@@ -723,9 +676,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float g1 = (colmul ? a.y * fg[2 * i + 1] : a.y) * fin;
                 const float u0 = (colmul ? b2.x * fu[2 * i] : b2.x) * fin;
                 const float u1 = (colmul ? b2.y * fu[2 * i + 1] : b2.y) * fin;
-                o[2 * i] = silu(g0) * u0;
-                o[2 * i + 1] = silu(g1) * u1;
+                if constexpr (kEpi) {
+                  o[2 * i] = g0;
+                  o[2 * i + 1] = g1;
+                  ov[2 * i] = u0;
+                  ov[2 * i + 1] = u1;
+                } else {
+                  o[2 * i] = silu(g0) * u0;
+                  o[2 * i + 1] = silu(g1) * u1;
+                }
               }
+              if constexpr (kEpi) epi_swiglu(p, t.g, orow, t.ct * 128 + h * 64 + c * 32, o, ov);
               emit(t.ct * 128 + h * 64 + c * 32, o);
             }
           } else {
@@ -744,6 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 o[2 * i] = a.x * fin;
                 o[2 * i + 1] = a.y * fin;
               }
+              if constexpr (kEpi) epi_apply(p, t.g, orow, col, o);
               emit(col, o);
             }
           }
@@ -796,15 +758,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               const float *fg = cf + colt(c), *fu = cf + colt(c + 2);
-              float o[32];
+              float o[32], ov[kEpi ? 32 : 1];
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
                 const float2 a = acc[c * 16 + i], b2 = acc[(c + 2) * 16 + i];
                 const float gs0 = need_col ? fg[2 * i] : 1.0f, gs1 = need_col ? fg[2 * i + 1] : 1.0f;
                 const float us0 = need_col ? fu[2 * i] : 1.0f, us1 = need_col ? fu[2 * i + 1] : 1.0f;
-                o[2 * i] = silu(a.x * s0 * gs0) * (b2.x * s0 * us0);
-                o[2 * i + 1] = silu(a.y * s0 * gs1) * (b2.y * s0 * us1);
+                if constexpr (kEpi) {
+                  o[2 * i] = a.x * s0 * gs0;
+                  o[2 * i + 1] = a.y * s0 * gs1;
+                  ov[2 * i] = b2.x * s0 * us0;
+                  ov[2 * i + 1] = b2.y * s0 * us1;
+                } else {
+                  o[2 * i] = silu(a.x * s0 * gs0) * (b2.x * s0 * us0);
+                  o[2 * i + 1] = silu(a.y * s0 * gs1) * (b2.y * s0 * us1);
+                }
               }
+              if constexpr (kEpi) epi_swiglu(p, t.g, orow, t.ct * 128 + h * 64 + c * 32, o, ov);
               emit(t.ct * 128 + h * 64 + c * 32, o);
             }
           } else {
@@ -819,6 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 o[2 * i] = a.x * s0 * (need_col ? cf[colt(c) + 2 * i] : 1.0f);
                 o[2 * i + 1] = a.y * s0 * (need_col ? cf[colt(c) + 2 * i + 1] : 1.0f);
               }
+              if constexpr (kEpi) epi_apply(p, t.g, orow, col, o);
               emit(col, o);
             }
           }
@@ -844,12 +815,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (sw) {
             if (row_ok) {
               const float *fg = cf + colt(ca), *fu = cf + colt(cb);
-              float o[32];
+              float o[32], ov[kEpi ? 32 : 1];
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
                 const float gs = need_col ? fg[i] : 1.0f, us = need_col ? fu[i] : 1.0f;
-                o[i] = silu(__uint_as_float(va[i]) * s0 * gs) * (__uint_as_float(vb[i]) * s0 * us);
+                if constexpr (kEpi) {
+                  o[i] = __uint_as_float(va[i]) * s0 * gs;
+                  ov[i] = __uint_as_float(vb[i]) * s0 * us;
+                } else {
+                  o[i] = silu(__uint_as_float(va[i]) * s0 * gs) * (__uint_as_float(vb[i]) * s0 * us);
+                }
               }
+              if constexpr (kEpi) epi_swiglu(p, t.g, orow, t.ct * 128 + h * 64 + cp * 32, o, ov);
               emit(t.ct * 128 + h * 64 + cp * 32, o);
             }
             continue;
@@ -866,6 +843,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float cs1 = need_col ? cf[colt(c) + i] : 1.0f;
               o[i] = __uint_as_float(vv[i]) * s0 * cs1;
             }
+            if constexpr (kEpi) epi_apply(p, t.g, orow, col, o);
             emit(col, o);
           }
         }
@@ -893,6 +871,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + (r * p.ld_out) * esz + c * 16) =
             make_uint4(0, 0, 0, 0);
       }
+      if constexpr (kEpi) {  // the kept pre-activations too
+        const int64_t zc = p.ncols / 8, zn = p.preact ? (static_cast<int64_t>(p.M) - tail0) * zc : 0;
+        for (int64_t i = static_cast<int64_t>(blockIdx.x) * kEpiThreads + et; i < zn;
+             i += static_cast<int64_t>(gridDim.x) * kEpiThreads)
+          reinterpret_cast<uint4 *>(p.preact)[tail0 * zc + i] = make_uint4(0, 0, 0, 0);
+      }
     }
   }
 
@@ -916,10 +900,10 @@ int num_sms() {
   return g_num_sms;
 }
 
-template <int kElem, bool kBMN, bool kPromote, int kMode>
+template <int kElem, bool kBMN, bool kPromote, int kMode, bool kEpi = false>
 static cudaError_t launch_inst(const CUtensorMap &tmA, const CUtensorMap &tmB, const CUtensorMap &tmOut,
                                const GemmParams &p, int grid, cudaStream_t st) {
-  auto kern = gmm_tc_kernel<kElem, kBMN, kPromote, kMode>;
+  auto kern = gmm_tc_kernel<kElem, kBMN, kPromote, kMode, kEpi>;
   const size_t smem = gemm_smem_bytes<kMode>();
   cudaFuncAttributes attr;
   cudaError_t e = cudaFuncGetAttributes(&attr, kern);
@@ -934,6 +918,27 @@ static cudaError_t launch_inst(const CUtensorMap &tmA, const CUtensorMap &tmB, c
   return cudaGetLastError();
 }
 
+// the row passes (forward, dlhs); kEpi: with bias, activation and residual
+template <bool kEpi>
+static cudaError_t launch_rows(const GemmConfig &cfg, const CUtensorMap &tmA, const CUtensorMap &tmB,
+                               const CUtensorMap &tmOut, const GemmParams &p, int grid, cudaStream_t st) {
+  if (cfg.mode == MODE_ROWS_BLK) {  // block-wise rhs scales: promoted fp8 only
+    if (cfg.elem_bytes != 1 || !cfg.promote) return cudaErrorInvalidValue;
+    return cfg.b_mn_major ? launch_inst<1, true, true, MODE_ROWS_BLK, kEpi>(tmA, tmB, tmOut, p, grid, st)
+                          : launch_inst<1, false, true, MODE_ROWS_BLK, kEpi>(tmA, tmB, tmOut, p, grid, st);
+  }
+  if (cfg.elem_bytes == 1) {
+    if (cfg.b_mn_major)
+      return cfg.promote ? launch_inst<1, true, true, MODE_ROWS, kEpi>(tmA, tmB, tmOut, p, grid, st)
+                         : launch_inst<1, true, false, MODE_ROWS, kEpi>(tmA, tmB, tmOut, p, grid, st);
+    return cfg.promote ? launch_inst<1, false, true, MODE_ROWS, kEpi>(tmA, tmB, tmOut, p, grid, st)
+                       : launch_inst<1, false, false, MODE_ROWS, kEpi>(tmA, tmB, tmOut, p, grid, st);
+  }
+  if (cfg.promote) return cudaErrorInvalidValue;
+  return cfg.b_mn_major ? launch_inst<2, true, false, MODE_ROWS, kEpi>(tmA, tmB, tmOut, p, grid, st)
+                        : launch_inst<2, false, false, MODE_ROWS, kEpi>(tmA, tmB, tmOut, p, grid, st);
+}
+
 cudaError_t launch_gemm(const GemmConfig &cfg, const CUtensorMap &tmA, const CUtensorMap &tmB,
                         const CUtensorMap &tmOut, const GemmParams &p, int grid, cudaStream_t st) {
   if (cfg.cta_pairs) return launch_gemm_pair(cfg, tmA, tmB, tmOut, p, grid, st);
@@ -944,21 +949,8 @@ cudaError_t launch_gemm(const GemmConfig &cfg, const CUtensorMap &tmA, const CUt
     if (cfg.elem_bytes == 2 && !cfg.promote) return launch_inst<2, false, false, MODE_TGMM>(tmA, tmB, tmOut, p, grid, st);
     return cudaErrorInvalidValue;
   }
-  if (cfg.mode == MODE_ROWS_BLK) {  // block-wise rhs scales: promoted fp8 only
-    if (cfg.elem_bytes != 1 || !cfg.promote) return cudaErrorInvalidValue;
-    return cfg.b_mn_major ? launch_inst<1, true, true, MODE_ROWS_BLK>(tmA, tmB, tmOut, p, grid, st)
-                          : launch_inst<1, false, true, MODE_ROWS_BLK>(tmA, tmB, tmOut, p, grid, st);
-  }
-  if (cfg.elem_bytes == 1) {
-    if (cfg.b_mn_major)
-      return cfg.promote ? launch_inst<1, true, true, MODE_ROWS>(tmA, tmB, tmOut, p, grid, st)
-                         : launch_inst<1, true, false, MODE_ROWS>(tmA, tmB, tmOut, p, grid, st);
-    return cfg.promote ? launch_inst<1, false, true, MODE_ROWS>(tmA, tmB, tmOut, p, grid, st)
-                       : launch_inst<1, false, false, MODE_ROWS>(tmA, tmB, tmOut, p, grid, st);
-  }
-  if (cfg.promote) return cudaErrorInvalidValue;
-  return cfg.b_mn_major ? launch_inst<2, true, false, MODE_ROWS>(tmA, tmB, tmOut, p, grid, st)
-                        : launch_inst<2, false, false, MODE_ROWS>(tmA, tmB, tmOut, p, grid, st);
+  return cfg.epilogue ? launch_rows<true>(cfg, tmA, tmB, tmOut, p, grid, st)
+                      : launch_rows<false>(cfg, tmA, tmB, tmOut, p, grid, st);
 }
 
 }  // namespace gmm

@@ -110,6 +110,13 @@ struct GemmParams {
   int swiglu_f;               // MODE_ROWS forward: F > 0 fuses SwiGLU over the merged
                               // columns [0, F) gate | [F, 2F) up and writes [M, F];
                               // 0 writes the plain product
+  // fused epilogue (GemmConfig::epilogue, row passes): out = act(z) + residual
+  // with z = product + bias[g]
+  const float *bias;          // [G][ncols], or NULL
+  const void *residual;       // rows of pitch ld_out, f32 or bf16, or NULL
+  int res_f32;
+  void *preact;               // bf16 [M][ncols] receives z, or NULL
+  int act;                    // gmm_act (SwiGLU: swiglu_f > 0)
   int tg_rows_fastest;        // MODE_TGMM item order within a group: 1 = row tiles (dout
                               // columns) fastest, each lhs column tile reused by
                               // consecutive items; 0 = column tiles fastest
@@ -126,6 +133,7 @@ struct GemmConfig {
                     // the B tensor map's K-major box is then tile_n / 2 rows
   int tile_n;       // tile columns: 256, or 128 (CTA pairs, promoted E4M3,
                     // K-major B: four TMEM accumulator buffers)
+  bool epilogue;    // row passes: bias, kept z, activation, residual (GemmParams)
 };
 
 int num_sms();

@@ -327,6 +327,211 @@ def gmm_backward(lhs: torch.Tensor, dout: torch.Tensor, rhs: torch.Tensor, rhs_s
     return dlhs, drhs
 
 
+ACTS = {"none": B.ACT_NONE, "relu": B.ACT_RELU, "silu": B.ACT_SILU, "gelu": B.ACT_GELU,
+        "gelu_tanh": B.ACT_GELU_TANH, "swiglu": B.ACT_SWIGLU}
+SCORES = {"softmax": B.SCORE_SOFTMAX, "sigmoid": B.SCORE_SIGMOID}
+
+
+def _name(table: dict, name, what: str) -> int:
+    if name not in table:
+        raise ValueError(f"{what} must be one of {sorted(table)}, not {name!r}")
+    return table[name]
+
+
+def _same_device(first: torch.Tensor, **others):
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, expected {first.device}")
+
+
+def _shape(t: torch.Tensor | None, name: str, shape):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _scratch(ws: torch.Tensor | None, nbytes: int, device) -> torch.Tensor:
+    """The caller's workspace, or one from torch's caching allocator for this
+    call alone: the allocator keeps it apart per stream and per captured
+    graph, so that calls on several streams or in several graphs share none."""
+    return ws if ws is not None else torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+
+
+def gmm_fwd_act(lhs: torch.Tensor, rhs: torch.Tensor, rhs_scales: torch.Tensor | None, group_sizes: torch.Tensor,
+                act: str = "none", bias: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+                rule="static", static_scale: torch.Tensor | None = None, transpose_rhs: bool = False,
+                out_dtype=torch.bfloat16, out: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                lhs_scales: torch.Tensor | None = None, keep_preact: bool = False,
+                preact: torch.Tensor | None = None):
+    """gmm_fwd with bias, activation and residual in the epilogue:
+    out = act(z) + residual, z = product + bias[g].  ``act``: "none", "relu",
+    "silu", "gelu", "gelu_tanh" or "swiglu" (merged gate|up rhs; out is
+    [M, N/2]).  bias: fp32 [G, N]; residual: bf16 or fp32, of out's shape (it
+    may be ``out`` itself when of its type).  With keep_preact (or a bf16
+    [M, N] buffer ``preact``) returns (out, z), z for gmm_act_bwd.  Other
+    arguments as for gmm_fwd."""
+    a_code = _name(ACTS, act, "act")
+    M, K = lhs.shape
+    G, K2, N = (rhs.shape[0], rhs.shape[2], rhs.shape[1]) if transpose_rhs else rhs.shape
+    if K2 != K:
+        raise ValueError(f"lhs contracts over {K}, rhs over {K2}")
+    r = _rule(rule)
+    out_shape = (M, N // 2 if act == "swiglu" else N)
+    _shape(bias, "bias", (G, N))
+    _shape(residual, "residual", out_shape)
+    _shape(out, "out", out_shape)
+    _shape(preact, "preact", (M, N))
+    _shape(group_sizes, "group_sizes", (G,))
+    _same_device(lhs, rhs=rhs, rhs_scales=rhs_scales, group_sizes=group_sizes, bias=bias, residual=residual, out=out,
+                 ws=ws, preact=preact, static_scale=static_scale, lhs_scales=lhs_scales)
+    if lhs.dtype in (torch.uint8, torch.float8_e4m3fn):
+        sc = static_scale if r == B.Q_STATIC else lhs_scales
+        a = _operand(_dev(lhs, "lhs"), B.DT_E4M3, _dev(sc, "lhs scale", torch.float32), r)
+    else:
+        a = _operand(_dev(lhs, "lhs", torch.bfloat16), B.DT_BF16, _dev(static_scale, "static_scale", torch.float32), r)
+    if preact is None and keep_preact:
+        preact = torch.empty((M, N), dtype=torch.bfloat16, device=lhs.device)
+    if out is None:
+        out = torch.empty(out_shape, dtype=out_dtype, device=lhs.device)
+    epi = B.Epilogue(a_code, _dev(bias, "bias", torch.float32),
+                     _dev(residual, "residual", (torch.bfloat16, torch.float32)),
+                     _TORCH_DT[residual.dtype] if residual is not None else B.DT_BF16,
+                     _dev(preact, "preact", torch.bfloat16))
+    with torch.cuda.device(lhs.device):
+        ws = _scratch(ws, gmm_workspace_bytes(B.OP_FWD, M, K, N, G), lhs.device)
+        st = B.lib().gmm_fwd_act(a, _rhs_operand(rhs, rhs_scales), int(transpose_rhs),
+                                 _dev(group_sizes, "group_sizes", torch.int32), G, M, K, N, ctypes.byref(epi),
+                                 _dev(out, "out", (torch.bfloat16, torch.float32)), _TORCH_DT[out.dtype],
+                                 _dev(ws, "ws"), ws.numel(), _stream(lhs))
+    _check(st, "gmm_fwd_act")
+    return out if preact is None else (out, preact)
+
+
+def gmm_act_bwd(dout: torch.Tensor, preact: torch.Tensor, group_sizes: torch.Tensor, act: str = "none",
+                with_dbias: bool = True, dz: torch.Tensor | None = None, dbias: torch.Tensor | None = None,
+                ws: torch.Tensor | None = None):
+    """Gradient of gmm_fwd_act's epilogue: (dz [M, N] bf16, dbias [G, N] fp32
+    or None).  dz = dout * act'(z) is the dout of gmm_dlhs / tgmm_drhs /
+    gmm_backward; the residual's gradient is dout itself."""
+    a_code = _name(ACTS, act, "act")
+    M, N = preact.shape
+    G = int(group_sizes.numel())
+    _shape(dout, "dout", (M, N // 2 if act == "swiglu" else N))
+    _shape(dz, "dz", (M, N))
+    _shape(dbias, "dbias", (G, N))
+    _same_device(dout, preact=preact, group_sizes=group_sizes, dz=dz, dbias=dbias, ws=ws)
+    if dz is None:
+        dz = torch.empty((M, N), dtype=torch.bfloat16, device=dout.device)
+    if dbias is None and with_dbias:
+        dbias = torch.empty((G, N), dtype=torch.float32, device=dout.device)
+    with torch.cuda.device(dout.device):
+        ws = _scratch(ws, int(B.lib().gmm_act_bwd_workspace_bytes(M, N, G)), dout.device)
+        st = B.lib().gmm_act_bwd(_dev(dout, "dout", torch.bfloat16), _dev(preact, "preact", torch.bfloat16), a_code,
+                                 _dev(group_sizes, "group_sizes", torch.int32), G, M, N,
+                                 _dev(dz, "dz", torch.bfloat16), _dev(dbias, "dbias", torch.float32), _dev(ws, "ws"),
+                                 ws.numel(), _stream(dout))
+    _check(st, "gmm_act_bwd")
+    return dz, dbias
+
+
+def gmm_moe_few(x: torch.Tensor, expert_ids: torch.Tensor, weights: torch.Tensor, w1: torch.Tensor,
+                w1_scales: torch.Tensor | None, w2: torch.Tensor, w2_scales: torch.Tensor | None,
+                transpose_rhs: bool = False, out_dtype=torch.bfloat16, out: torch.Tensor | None = None,
+                ws: torch.Tensor | None = None):
+    """A whole mixture-of-experts layer for a few tokens in one kernel:
+    y[t] = sum_j weights[t, j] * (silu(g) * u) @ W2[e], [g | u] = x[t] @ W1[e],
+    e = expert_ids[t, j].  x: bf16 [T, K] (not quantized); expert_ids int32
+    and weights fp32 [T, k] (as gmm_router_topk gives them); w1 [G, K, 2F]
+    merged gate|up and w2 [G, F, N] (transpose_rhs: [G, 2F, K], [G, N, F]),
+    both E4M3 codes with scales [G, 2F] and [G, N], or both bf16 with scales
+    None.  T * k <= 1024.  Returns y [T, N]."""
+    T, K = x.shape
+    k = expert_ids.shape[1]
+    G, K2, F2 = (w1.shape[0], w1.shape[2], w1.shape[1]) if transpose_rhs else w1.shape
+    G2, F, N = (w2.shape[0], w2.shape[2], w2.shape[1]) if transpose_rhs else w2.shape
+    if K2 != K or G2 != G or F2 != 2 * F:
+        raise ValueError(f"x {tuple(x.shape)}, w1 {tuple(w1.shape)} and w2 {tuple(w2.shape)} do not fit together")
+    _shape(expert_ids, "expert_ids", (T, k))
+    _shape(weights, "weights", (T, k))
+    _shape(w1_scales, "w1_scales", (G, F2))
+    _shape(w2_scales, "w2_scales", (G, N))
+    _shape(out, "out", (T, N))
+    _same_device(x, expert_ids=expert_ids, weights=weights, w1=w1, w1_scales=w1_scales, w2=w2, w2_scales=w2_scales,
+                 out=out, ws=ws)
+    if w1.dtype not in _TORCH_DT or w2.dtype not in _TORCH_DT:
+        raise ValueError(f"w1 / w2 have dtype {w1.dtype} / {w2.dtype}, expected E4M3 codes or bf16")
+    dt = _TORCH_DT[w1.dtype]
+    if out is None:
+        out = torch.empty((T, N), dtype=out_dtype, device=x.device)
+    with torch.cuda.device(x.device):
+        ws = _scratch(ws, int(B.lib().gmm_moe_few_workspace_bytes(T, k, G, K, F, N, dt)), x.device)
+        st = B.lib().gmm_moe_few(
+            _dev(x, "x", torch.bfloat16), _dev(expert_ids, "expert_ids", torch.int32),
+            _dev(weights, "weights", torch.float32), T, k,
+            _operand(_dev(w1, "w1"), dt, _dev(w1_scales, "w1_scales", torch.float32), B.Q_NONE),
+            _operand(_dev(w2, "w2"), _TORCH_DT[w2.dtype], _dev(w2_scales, "w2_scales", torch.float32), B.Q_NONE),
+            int(transpose_rhs), G, K, F, N, _dev(out, "out", (torch.bfloat16, torch.float32)), _TORCH_DT[out.dtype],
+            _dev(ws, "ws"), ws.numel(), _stream(x))
+    _check(st, "gmm_moe_few")
+    return out
+
+
+def gmm_router_topk(logits: torch.Tensor, k: int, score: str = "softmax", select_bias: torch.Tensor | None = None,
+                    normalize: bool = False, scale: float = 1.0):
+    """The router: (expert_ids int32 [T, k], weights fp32 [T, k]) of the k
+    experts of largest score (+ select_bias, fp32 [E], for the choice only),
+    ties to the lowest index.  weights = scale * score, or with normalize
+    scale * score / (sum of the chosen scores).  Experts masked with -inf are
+    never chosen (id -1, weight 0 where fewer than k are left)."""
+    T, E = logits.shape
+    _shape(select_bias, "select_bias", (E,))
+    _same_device(logits, select_bias=select_bias)
+    ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
+    weights = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+    with torch.cuda.device(logits.device):
+        st = B.lib().gmm_router_topk(_dev(logits, "logits", (torch.float32, torch.bfloat16)), _TORCH_DT[logits.dtype],
+                                     T, E, k, _name(SCORES, score, "score"),
+                                     _dev(select_bias, "select_bias", torch.float32), int(normalize), float(scale),
+                                     ids.data_ptr(), weights.data_ptr(), _stream(logits))
+    _check(st, "gmm_router_topk")
+    return ids, weights
+
+
+def gmm_router_topk_bwd(dweights: torch.Tensor, logits: torch.Tensor, expert_ids: torch.Tensor,
+                        score: str = "softmax", normalize: bool = False, scale: float = 1.0):
+    """Gradient of gmm_router_topk's weights: dlogits [T, E] (logits' type)
+    from dweights [T, k] fp32, the logits and the chosen expert_ids."""
+    T, E = logits.shape
+    k = expert_ids.shape[1]
+    _shape(expert_ids, "expert_ids", (T, k))
+    _shape(dweights, "dweights", (T, k))
+    _same_device(logits, dweights=dweights, expert_ids=expert_ids)
+    dlogits = torch.empty_like(logits)
+    with torch.cuda.device(logits.device):
+        st = B.lib().gmm_router_topk_bwd(_dev(dweights, "dweights", torch.float32),
+                                         _dev(logits, "logits", (torch.float32, torch.bfloat16)),
+                                         _TORCH_DT[logits.dtype], _dev(expert_ids, "expert_ids", torch.int32), T, E, k,
+                                         _name(SCORES, score, "score"), int(normalize), float(scale),
+                                         dlogits.data_ptr(), _stream(logits))
+    _check(st, "gmm_router_topk_bwd")
+    return dlogits
+
+
+def gmm_combine_dweight(dy: torch.Tensor, rows: torch.Tensor, slot: torch.Tensor):
+    """Gradient of the combine's routing weights: dweight[t, j] =
+    sum_n dy[t, n] * rows[slot[t, j], n] (fp32 [T, k]; 0 for a slot outside
+    rows).  dy [T, N] and rows [R, N] bf16, slot int32 [T, k]."""
+    T, k = slot.shape
+    _shape(dy, "dy", (T, rows.shape[1]))
+    _same_device(dy, rows=rows, slot=slot)
+    dw = torch.empty((T, k), dtype=torch.float32, device=dy.device)
+    with torch.cuda.device(dy.device):
+        st = B.lib().gmm_combine_dweight(_dev(dy, "dy", torch.bfloat16), _dev(rows, "rows", torch.bfloat16),
+                                         rows.shape[0], _dev(slot, "slot", torch.int32), T, k, rows.shape[1],
+                                         dw.data_ptr(), _stream(dy))
+    _check(st, "gmm_combine_dweight")
+    return dw
+
+
 def gmm_read_device_status(ws: torch.Tensor):
     """(status, bits) left in ``ws`` by the last call; synchronizes the stream."""
     bits = ctypes.c_uint32(0)
