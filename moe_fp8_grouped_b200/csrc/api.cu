@@ -752,7 +752,7 @@ static ActBwdLayout act_bwd_layout(int64_t M, int64_t N, int32_t G) {
 // Workspace of gmm_moe_few: status header, bf16 rows between the products,
 // fp32 partial sums (of either product: the second overwrites the first's).
 struct FewLayout {
-  size_t h, partial, total;
+  size_t h, largest, partial, extra, total;
 };
 
 static gmm_status check_few(int64_t T, int32_t k, int32_t G, int64_t K, int64_t F, int64_t N) {
@@ -760,17 +760,20 @@ static gmm_status check_few(int64_t T, int32_t k, int32_t G, int64_t K, int64_t 
   if (K % kBlk || F % kBlk || N % kBlk) return GMM_ERR_SHAPE;
   if (T > kFewMaxPairs || k > kFewMaxPairs || T * k > kFewMaxPairs) return GMM_ERR_UNSUPPORTED;
   if (F > (1 << 19)) return GMM_ERR_UNSUPPORTED;
+  // units of either product (bf16 weights have the most) are counted in 31 bits
+  if (T * k * (K > N ? K : N) / kBlk > INT_MAX / (2 * F / 64)) return GMM_ERR_UNSUPPORTED;
   const gmm_status s = check_sizes(1, K, 2 * F, G);
   return s != GMM_OK ? s : check_sizes(1, F, N, G);
 }
 
-static FewLayout few_layout(int64_t T, int32_t k, int64_t K, int64_t F, int64_t N, int elem) {
-  const int64_t pairs = T * k, bke = kBlk / elem;
-  const int64_t p1 = few_parts(2 * F / kBlk, K / bke) * 2 * F, p2 = few_parts(N / kBlk, F / bke) * N;
+static FewLayout few_layout(int64_t T, int32_t k, int64_t F, int64_t N) {
+  const int64_t pairs = T * k, cols = 2 * F > N ? 2 * F : N;
   FewLayout L;
   L.h = sizeof(WsHeader);
-  L.partial = L.h + align256(static_cast<size_t>(pairs) * F * 2);
-  L.total = L.partial + align256(sizeof(float) * static_cast<size_t>(pairs) * (p1 > p2 ? p1 : p2));
+  L.largest = L.h + align256(static_cast<size_t>(pairs) * F * 2);
+  L.partial = L.largest + align256(sizeof(uint32_t) * static_cast<size_t>(T + pairs));
+  L.extra = L.partial + align256(sizeof(float) * static_cast<size_t>(pairs) * cols);
+  L.total = L.extra + align256(sizeof(float) * few_extra_floats(T));
   return L;
 }
 
@@ -836,7 +839,7 @@ gmm_status gmm_act_bwd(const void *dout_bf16, const void *preact_bf16, gmm_act a
 size_t gmm_moe_few_workspace_bytes(int64_t T, int32_t k, int32_t G, int64_t K, int64_t F, int64_t N,
                                    gmm_dtype weight_dtype) {
   if (check_few(T, k, G, K, F, N) != GMM_OK || (weight_dtype != GMM_E4M3 && weight_dtype != GMM_BF16)) return 0;
-  return few_layout(T, k, K, F, N, weight_dtype == GMM_E4M3 ? 1 : 2).total;
+  return few_layout(T, k, F, N).total;
 }
 
 gmm_status gmm_moe_few(const void *x_bf16, const int32_t *expert_ids, const float *weights, int64_t T, int32_t k,
@@ -855,7 +858,7 @@ gmm_status gmm_moe_few(const void *x_bf16, const int32_t *expert_ids, const floa
   if (!al16(x_bf16) || !al16(w1.data) || !al16(w2.data) || !al16(y) || !al16(ws) ||
       (elem == 1 && (!al16(w1.scale) || !al16(w2.scale))))
     return GMM_ERR_ALIGNMENT;
-  const FewLayout L = few_layout(T, k, K, F, N, elem);
+  const FewLayout L = few_layout(T, k, F, N);
   if (!ws || ws_bytes < L.total) return GMM_ERR_WORKSPACE;
   uint8_t *w = static_cast<uint8_t *>(ws);
   const bool mn = transpose_rhs == 0;
@@ -874,7 +877,9 @@ gmm_status gmm_moe_few(const void *x_bf16, const int32_t *expert_ids, const floa
   p.s1 = elem == 1 ? w1.scale : nullptr;
   p.s2 = elem == 1 ? w2.scale : nullptr;
   p.h = reinterpret_cast<__nv_bfloat16 *>(w + L.h);
+  p.largest = reinterpret_cast<uint32_t *>(w + L.largest);
   p.partial = reinterpret_cast<float *>(w + L.partial);
+  p.extra = reinterpret_cast<float *>(w + L.extra);
   p.y = y;
   p.T = static_cast<int>(T);
   p.k = k;

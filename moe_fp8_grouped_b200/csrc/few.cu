@@ -8,12 +8,15 @@
 // HBM and everything else must hide behind it.
 //
 // Split.  The weights of the active experts are cut into units of 128 columns
-// x 128 bytes of contraction (16 KB).  The units of both products are numbered
-// (expert, column tile, contraction block) and every CTA takes one contiguous
-// range of equal length, so all SMs stream the same number of bytes whatever
-// the routing.  A column tile whose units fall into several ranges gets one
-// fp32 partial sum from each CTA; the partials are added in CTA order, so the
-// result does not depend on timing.
+// x 128 bytes of contraction (16 KB).  As many column tiles as fill whole waves
+// of CTAs go one to a CTA; the contraction of the tiles left over is cut into
+// slices (at most 16) so that every SM streams nearly the same number of
+// bytes whatever the routing.  CTAs that run side by side read neighbouring
+// tiles at the same depth, which for [G, K, N] weights is neighbouring memory
+// (a copy-only version of this stream ran 41 us for 235 MB in this order and
+// 55 us with contiguous unit ranges per CTA).  A sliced tile gets one fp32
+// partial sum per slice, added in slice order, so the result does not depend
+// on timing.
 //
 // Tile.  The weights are the 128-row operand of tcgen05.mma and stay in the
 // layout they have in memory (MN-major for [G, K, N], K-major for [G, N, K]):
@@ -22,12 +25,14 @@
 // groups) are the MMA's columns.
 //
 // Activations stay bf16 in precision although the MMA multiplies E4M3: a bf16
-// value has 8 significant bits, so scaled by a power of two (one per row and
-// block of 128, from the block's largest magnitude, put into [128, 256)) it is
-// hi + lo / 16 with two E4M3 values of 4 significant bits each, exactly for
-// values down to 2^-13 of the block's largest and within 2^-22 of that largest
-// below.  hi and lo are separate MMA columns and are joined, unscaled and
-// summed in fp32 by the epilogue, one block at a time.  bf16 weights multiply
+// value has 8 significant bits, so scaled by a power of two (one per row, that
+// puts the row's largest magnitude into [128, 256)) it is hi + lo / 16 with two
+// E4M3 values of 4 significant bits each, exactly for values down to 2^-13 of
+// the row's largest and within 2^-22 of that largest below.  hi and lo are
+// separate MMA columns, joined and unscaled once per tile.  (A scale per block
+// of 128 instead would need every block's accumulator read and scaled on its
+// own: measured, that epilogue took 500 to 1000 cycles a unit and was the
+// bound.)  bf16 weights multiply
 // the bf16 rows as they are.
 //
 // The layer is one cooperative launch: gate|up product, grid barrier, SwiGLU
@@ -36,8 +41,14 @@
 // the down product's first copies before the barriers, so HBM keeps working
 // across them.
 //
-// Warps (320 threads, one CTA per SM): 0 TMA producer, 1 MMA issuer and TMEM
-// owner, 2-5 activation loaders, 6-9 epilogue (TMEM lanes 32 (w % 4) ..).
+// Warps (512 threads, one CTA per SM): 0-1 TMA producers, 2-3 MMA issuers (2
+// owns the TMEM), 4-11 activation loaders, 12-15 epilogue (TMEM lanes 32 (w %
+// 4) ..).  Producers and issuers take alternate units: one thread's wait and
+// issue per unit bounds the stream below HBM (copies alone: 51 us against 41
+// us with two).  Each issuer sums its units of a tile in an accumulator of its
+// own; the epilogue adds the two.  A loader warp prepares every eighth unit on
+// its own, so that eight units' loads are in flight: under the weight stream
+// one takes 1000 to 2000 cycles, a unit's share of HBM 670.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -49,21 +60,25 @@
 namespace gmm {
 namespace {
 
-constexpr int kFewThreads = 320;
+constexpr int kFewThreads = 512;
+constexpr int kFewMaxSlices = 16;
+constexpr int kFewOwnTokens = 30;  // rows whose largest value every CTA finds on its own
 constexpr int kUnitBytes = 16384;  // 128 columns x 128 bytes of contraction
-constexpr int kLoadWarp0 = 2, kLoadWarps = 4;
-constexpr int kFewEpiWarp0 = 6, kFewEpiWarps = 4;
+constexpr int kProdWarps = 2;                // warps 0 .. 1
+constexpr int kMmaWarp0 = 2, kMmaWarps = 2;
+constexpr int kLoadWarp0 = 4, kLoadWarps = 8;
+constexpr int kFewEpiWarp0 = 12, kFewEpiWarps = 4;
 
-// rows of a group, stages and TMEM buffers of the two variants
+// stages and tile accumulators in flight of the two variants
 template <int kRows>
 struct FewCfg;
 template <>
 struct FewCfg<8> {
-  static constexpr int kStages = 11, kBufs = 8, kAhead = 4;
+  static constexpr int kStages = 10, kBufs = 4;
 };
 template <>
 struct FewCfg<32> {
-  static constexpr int kStages = 8, kBufs = 4, kAhead = 2;
+  static constexpr int kStages = 8, kBufs = 2;
 };
 
 template <int kRows>
@@ -73,18 +88,21 @@ constexpr int few_b_bytes() { return 2 * kRows * 128; }  // hi rows and lo rows
 template <int kRows>
 struct FewTail {
   using C = FewCfg<kRows>;
-  static constexpr int kRing = C::kStages + C::kBufs;
-  uint64_t full_a[C::kStages], full_b[C::kStages], empty[C::kStages];
-  uint64_t tfull[C::kBufs], tempty[C::kBufs];
-  uint64_t sfull[kRing];
-  uint64_t drain;
+  // stage s: weights landed; weights landed and rows written; MMAs done
+  uint64_t full_a[C::kStages], full[C::kStages], done[C::kStages];
+  // accumulator b: sums of issuer i complete; read
+  uint64_t tfull[C::kBufs][kMmaWarps], tempty[C::kBufs];
+  uint64_t drain[kMmaWarps];
+  int last[C::kStages];  // the stage's newest copy (unit), -1: none
   uint32_t tmem_slot;
   int abort_flag, no_abort, ngroups;
-  float inv_scale[kRing][kRows];
+  int slices[2];  // of each product's tiles left over
+  float up[kFewMaxPairs];            // power of two that scales each pair's row (E4M3)
   int cnt[kMaxGroups];               // rows per expert, then group offset
   uint16_t first[kMaxGroups];        // first entry of the expert in rows[]
   uint16_t rows[kFewMaxPairs];       // pairs sorted by expert
   uint16_t pos[kFewMaxPairs];        // rank of each pair within its expert
+  uint16_t token[kFewMaxPairs];      // token of each pair
   int16_t pair_group[kFewMaxPairs];  // group of each pair, -1: none
   uint16_t g_expert[kFewMaxPairs], g_first[kFewMaxPairs], g_count[kFewMaxPairs];
   int ids[kFewMaxPairs];
@@ -96,46 +114,80 @@ constexpr size_t few_smem_bytes() {
          sizeof(FewTail<kRows>);
 }
 
-// One of the two products as a list of units, and this CTA's range of it.
+// One of the two products: `tiles` column tiles per group, kb contraction
+// blocks.  The tiles of all groups are numbered; the first waves * gridDim.x go
+// whole to CTA (number % gridDim.x), the `left` others as `slices` slices of
+// their contraction, item (slice, tile) to CTA (item number % gridDim.x).
 struct Product {
-  int tiles, kb;           // column tiles of 128, contraction blocks
-  uint64_t total, lo, hi;  // units; this CTA's [lo, hi)
-  uint32_t grid;           // CTAs that have units
+  int tiles, kb, waves, left, slices;
+  int n, items;  // this CTA's units, and the items (tiles or slices) they belong to
   __device__ __forceinline__ void init(int ngroups, int tiles_, int kb_) {
     tiles = tiles_;
     kb = kb_;
-    total = static_cast<uint64_t>(ngroups) * tiles * kb;
-    // CTAs with work: with fewer units than CTAs the first `total` take one
-    // each, so that the CTAs of a tile are always consecutive
-    grid = static_cast<uint32_t>(min(static_cast<uint64_t>(gridDim.x), total));
-    lo = hi = 0;
-    if (blockIdx.x < grid) {
-      lo = total * blockIdx.x / grid;
-      hi = total * (blockIdx.x + 1) / grid;
-    }
+    const int grid = gridDim.x, total = ngroups * tiles;
+    waves = total / grid;
+    left = total - waves * grid;
   }
-  // the CTA whose range holds unit u: the largest c with total * c / grid <= u
-  __device__ __forceinline__ uint32_t cta_of(uint64_t u) const {
-    return static_cast<uint32_t>(((u + 1) * grid - 1) / total);
+  // slices that make the CTA with the most units have the fewest (of those the
+  // smallest count): one candidate per lane, the first 16 lanes
+  __device__ __forceinline__ int best_slices(int lane) const {
+    const int c = lane + 1, grid = gridDim.x;
+    unsigned cost = 0xffffffffu;
+    if (c <= kFewMaxSlices && c <= kb)
+      cost = static_cast<unsigned>((left * c + grid - 1) / grid) * ((kb + c - 1) / c) * 32u + c;
+    return static_cast<int>(__reduce_min_sync(0xffffffffu, cost) & 31u);
+  }
+  __device__ __forceinline__ int slice_begin(int i) const { return i * kb / slices; }
+  __device__ __forceinline__ void count(int slices_) {
+    slices = slices_;
+    n = waves * kb;
+    items = waves;
+    for (int j = blockIdx.x; j < left * slices; j += gridDim.x) {
+      const int i = j / left;
+      n += slice_begin(i + 1) - slice_begin(i);
+      ++items;
+    }
   }
 };
 
-// Position in a product's unit list, advanced one unit at a time.
+// Position in this CTA's units of a product.
 struct Cursor {
-  int group, tile, kblk;
-  __device__ __forceinline__ void seek(const Product &p, uint64_t u) {
-    kblk = static_cast<int>(u % p.kb);
-    const uint64_t gt = u / p.kb;
-    tile = static_cast<int>(gt % p.tiles);
-    group = static_cast<int>(gt / p.tiles);
+  int item;              // waves first, then the CTA's slice items
+  int group, tile;       // column tile `tile` of group `group`
+  int kblk, kend;        // contraction block, end of the item's
+  int left_tile, slice;  // number among the tiles left over (-1: a whole tile)
+  __device__ __forceinline__ void open(const Product &p) {
+    int gt, k0 = 0;
+    kend = p.kb;
+    slice = 0;
+    left_tile = -1;
+    if (item < p.waves) {
+      gt = item * gridDim.x + blockIdx.x;
+    } else {
+      const int j = (item - p.waves) * gridDim.x + blockIdx.x;
+      slice = j / p.left;
+      left_tile = j - slice * p.left;
+      gt = p.waves * gridDim.x + left_tile;
+      k0 = p.slice_begin(slice);
+      kend = p.slice_begin(slice + 1);
+    }
+    group = gt / p.tiles;
+    tile = gt - group * p.tiles;
+    kblk += k0;
   }
-  __device__ __forceinline__ void next(const Product &p) {
-    if (++kblk == p.kb) {
-      kblk = 0;
-      if (++tile == p.tiles) {
-        tile = 0;
-        ++group;
-      }
+  // to unit `u` of the CTA (u < p.n)
+  __device__ __forceinline__ void seek(const Product &p, int u) {
+    item = 0;
+    kblk = 0;
+    open(p);
+    if (u) next(p, u);
+  }
+  __device__ __forceinline__ void next(const Product &p, int by = 1) {
+    kblk += by;
+    while (kblk >= kend) {
+      kblk -= kend;
+      ++item;
+      open(p);
     }
   }
 };
@@ -154,33 +206,40 @@ __device__ __forceinline__ float2 e4m3x2_to_f32(uint16_t c) {
   return __half22float2(*reinterpret_cast<__half2 *>(&h));
 }
 
-// Four bf16 values of a row's 128-block (the warp's lanes hold the block) as
-// E4M3 hi and lo codes; returns the factor that undoes the scaling.  A value
-// that is not finite becomes NaN.
-__device__ __forceinline__ float split_e4m3(const uint2 &raw, uint32_t &hi, uint32_t &lo) {
+// Power of two that puts a row's largest finite magnitude (as fp32 bits) into
+// [128, 256); at most 2^126, so that its inverse stays normal.
+__device__ __forceinline__ float row_scale_up(uint32_t largest) {
+  const int e = largest == 0 ? 0 : min(134 - static_cast<int>(largest >> 23), 126);
+  return __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+}
+
+__device__ __forceinline__ float inverse_of_power(float up) {
+  return __uint_as_float(0x7f000000u - __float_as_uint(up));  // 2^-e of 2^e
+}
+
+// |x| as fp32 bits, 0 when x is not finite
+__device__ __forceinline__ uint32_t finite_bits(float x) {
+  const uint32_t a = __float_as_uint(x) & 0x7fffffffu;
+  return a >= 0x7f800000u ? 0u : a;
+}
+
+// Four bf16 values, scaled, as E4M3 hi and lo codes.  A value that is not
+// finite becomes NaN.
+__device__ __forceinline__ void split_e4m3(const uint2 &raw, float up, uint32_t &hi, uint32_t &lo) {
   const __nv_bfloat162 *b = reinterpret_cast<const __nv_bfloat162 *>(&raw);
   const float2 p0 = __bfloat1622float2(b[0]), p1 = __bfloat1622float2(b[1]);
   float v[4] = {p0.x, p0.y, p1.x, p1.y};
-  uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t a = __float_as_uint(v[i]) & 0x7fffffffu;
-    if (a >= 0x7f800000u) v[i] = __uint_as_float(0x7fffffffu);
-    else m = max(m, a);
+    v[i] *= up;
+    if (!(fabsf(v[i]) <= 3.0e38f)) v[i] = __uint_as_float(0x7fffffffu);
   }
-  m = __reduce_max_sync(0xffffffffu, m);
-  // 2^s with largest * 2^s in [128, 256); s <= 126 so that 2^-s stays normal
-  const int s = m == 0 ? 0 : min(134 - static_cast<int>(m >> 23), 126);
-  const float up = __uint_as_float(static_cast<uint32_t>(127 + s) << 23);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] *= up;
   const uint16_t h0 = cvt_e4m3x2(v[0], v[1]), h1 = cvt_e4m3x2(v[2], v[3]);
   const float2 f0 = e4m3x2_to_f32(h0), f1 = e4m3x2_to_f32(h1);
   const uint16_t l0 = cvt_e4m3x2((v[0] - f0.x) * 16.0f, (v[1] - f0.y) * 16.0f);
   const uint16_t l1 = cvt_e4m3x2((v[2] - f1.x) * 16.0f, (v[3] - f1.y) * 16.0f);
   hi = h0 | (static_cast<uint32_t>(h1) << 16);
   lo = l0 | (static_cast<uint32_t>(l1) << 16);
-  return __uint_as_float(static_cast<uint32_t>(127 - s) << 23);
 }
 
 __device__ __forceinline__ float few_silu(float x) { return x / (1.0f + expf(-x)); }
@@ -191,13 +250,12 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                    const FewParams p) {
   using C = FewCfg<kRows>;
   using Tail = FewTail<kRows>;
-  constexpr int kSt = C::kStages, kBufs = C::kBufs, kRing = Tail::kRing;
+  constexpr int kSt = C::kStages, kBufs = C::kBufs;
   constexpr int kBBytes = few_b_bytes<kRows>();
   constexpr int kBKe = 128 / kElem;  // contraction elements per unit
-  constexpr int kBufCols = 2 * kRows;
-  constexpr int kTmem = kBufs * kBufCols < 32 ? 32 : kBufs * kBufCols;
-  constexpr int kRowsPerWarp = kRows / kLoadWarps;
-  static_assert((kTmem & (kTmem - 1)) == 0 && kTmem <= 512, "TMEM columns: a power of two");
+  constexpr int kBufCols = 2 * kRows;  // columns of one issuer's accumulator
+  constexpr int kTmem = kBufs * kMmaWarps * kBufCols;
+  static_assert((kTmem & (kTmem - 1)) == 0 && kTmem >= 32 && kTmem <= 512, "TMEM columns: a power of two");
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -207,20 +265,25 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   cooperative_groups::grid_group grid = cooperative_groups::this_grid();
 
   // ------------------------------------------------ set-up and row grouping
-  for (int i = tid; i < p.pairs; i += kFewThreads) t.ids[i] = p.ids[i];
+  for (int i = tid; i < p.pairs; i += kFewThreads) {
+    t.ids[i] = p.ids[i];
+    t.token[i] = static_cast<uint16_t>(i / p.k);
+  }
   for (int i = tid; i < p.G; i += kFewThreads) t.cnt[i] = 0;
+  if (kElem == 1 && blockIdx.x == 0)
+    for (int i = tid; i < p.pairs; i += kFewThreads) p.largest[p.T + i] = 0;  // of h, for the barrier after the first product
   if (tid == 0) {
     for (int i = 0; i < kSt; ++i) {
+      t.last[i] = -1;
       mbar_init(&t.full_a[i], 1);
-      mbar_init(&t.full_b[i], kLoadWarps);
-      mbar_init(&t.empty[i], 1);
+      mbar_init(&t.full[i], 1);
+      mbar_init(&t.done[i], 1);
     }
     for (int i = 0; i < kBufs; ++i) {
-      mbar_init(&t.tfull[i], 1);
+      for (int m = 0; m < kMmaWarps; ++m) mbar_init(&t.tfull[i][m], 1);
       mbar_init(&t.tempty[i], kFewEpiWarps);
     }
-    for (int i = 0; i < kRing; ++i) mbar_init(&t.sfull[i], kLoadWarps);
-    mbar_init(&t.drain, 1);
+    for (int i = 0; i < kMmaWarps; ++i) mbar_init(&t.drain[i], 1);
     t.abort_flag = 0;
     t.no_abort = 0;
     fence_barrier_init();
@@ -228,7 +291,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     tma_prefetch_desc(&tm2);
     if (blockIdx.x == 0) *p.status = 0;
   }
-  if (warp == 1) {
+  if (warp == kMmaWarp0) {
     tmem_alloc(&t.tmem_slot, kTmem);
     tmem_relinquish();
   }
@@ -236,6 +299,31 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = t.tmem_slot;
+  // largest magnitude of each token's row: every CTA on its own for few tokens,
+  // shared through memory and one more barrier for many
+  const bool share = kElem == 1 && p.T > kFewOwnTokens;
+  if (kElem == 1) {
+    const int step = share ? gridDim.x * 15 : 15;
+    for (int tok = share ? blockIdx.x * 15 + warp - 1 : warp - 1; warp > 0 && tok < p.T; tok += step) {
+      const uint4 *row = reinterpret_cast<const uint4 *>(p.x + static_cast<int64_t>(tok) * (p.kb1 * kBKe));
+      uint32_t m = 0;
+#pragma unroll 8
+      for (int i = lane; i < p.kb1 * kBKe / 8; i += 32) {
+        const uint4 v = row[i];
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          m = max(m, finite_bits(__uint_as_float(w[e] << 16)));
+          m = max(m, finite_bits(__uint_as_float(w[e] & 0xffff0000u)));
+        }
+      }
+      m = __reduce_max_sync(0xffffffffu, m);
+      if (lane == 0) {
+        if (share) p.largest[tok] = m;
+        else t.up[tok] = row_scale_up(m);
+      }
+    }
+  }
   if (warp == 0) {
     // rank of every pair within its expert, in pair order
     for (int base = 0; base < p.pairs; base += 32) {
@@ -276,7 +364,15 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       row0 += last & 0xffff;
       grp0 += last >> 16;
     }
-    if (lane == 0) t.ngroups = grp0;
+    Product a, b;
+    a.init(grp0, p.tiles1, p.kb1);
+    b.init(grp0, p.tiles2, p.kb2);
+    const int sa = a.best_slices(lane), sb = b.best_slices(lane);
+    if (lane == 0) {
+      t.ngroups = grp0;
+      t.slices[0] = sa;
+      t.slices[1] = sb;
+    }
   }
   __syncthreads();
   for (int q = tid; q < p.pairs; q += kFewThreads) {
@@ -287,80 +383,117 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   }
   __syncthreads();
 
+  if (share) grid.sync();
+  if (share) {
+    for (int i = tid; i < p.T; i += kFewThreads) t.up[i] = row_scale_up(__ldcg(p.largest + i));
+    __syncthreads();
+  }
   const WaitCtl ctl{p.wait_limit_ns, &t.abort_flag, p.status};
   const WaitCtl ctl_drain{p.wait_limit_ns, &t.no_abort, p.status};
-  Product prod[2];
-  prod[0].init(t.ngroups, p.tiles1, p.kb1);
-  prod[1].init(t.ngroups, p.tiles2, p.kb2);
-  const int n1 = static_cast<int>(prod[0].hi - prod[0].lo), n2 = static_cast<int>(prod[1].hi - prod[1].lo);
+  Product prod1, prod2;
+  prod1.init(t.ngroups, p.tiles1, p.kb1);
+  prod2.init(t.ngroups, p.tiles2, p.kb2);
+  prod1.count(t.slices[0]);
+  prod2.count(t.slices[1]);
+  const int n1 = prod1.n, n2 = prod2.n;
   // products with block scales (E4M3) use hi and lo columns, bf16 one column a row
   auto mma_cols = [&](int count) { return kElem == 1 ? 2 * ((count + 7) & ~7) : ((count + 15) & ~15); };
 
-  // per-role position over both products: units it = 0 .. n1 - 1 belong to the
-  // first product, n1 .. n1 + n2 - 1 to the second; a role that gave up a
-  // wait stops for good (ok = false) but still joins every barrier below
-  int it = 0;
+  // Units are numbered over both products: 0 .. n1 - 1 of the first, n1 ..
+  // n1 + n2 - 1 of the second; unit u uses stage u % kSt.  A role that gave up
+  // a wait stops for good (ok = false) but still joins every barrier below.
   bool ok = true;
+  int it = 0;            // producers: next unit of this warp; epilogue: next unit
+  int items = 0;         // items before the current product's (accumulator item g uses buffer g % kBufs)
+  uint32_t tphase = 0;   // epilogue: parity of each accumulator's next use
+  if (warp < kProdWarps) it = warp;
+  const uint64_t policy = l2_policy_evict_first();  // the weights are read once
 
-  // producer: copies until `stop`
-  Cursor pc;
-  auto produce = [&](int stop) {
-    for (; ok && it < stop; ++it) {
-      const int ph = it >= n1;
-      const Product &pr = prod[ph];
-      if (it == 0 || it == n1) pc.seek(pr, pr.lo);
+  // producer: the warp's copies of product `ph` up to unit `stop`
+  auto produce = [&](int ph, const Product &pr, int begin, int stop) {
+    const CUtensorMap *tm = ph ? &tm2 : &tm1;
+    if (!ok || it >= stop) return;
+    Cursor c{};
+    c.seek(pr, it - begin);
+    for (;;) {
       const int s = it % kSt;
-      if (!mbar_wait(&t.empty[s], ((it / kSt) & 1) ^ 1, ctl)) {
+      if (!mbar_wait(&t.done[s], ((it / kSt) & 1) ^ 1, ctl)) {
         ok = false;
-        break;
+        return;
       }
       mbar_arrive_expect_tx(&t.full_a[s], kUnitBytes);
-      const int e = t.g_expert[pc.group];
-      const CUtensorMap *tm = ph ? &tm2 : &tm1;
+      t.last[s] = it;
+      const int e = t.g_expert[c.group];
       uint8_t *dst = sA + s * kUnitBytes;
       if constexpr (kMN) {
-        const int y = e * (pr.kb * kBKe) + pc.kblk * kBKe;
+        const int y = e * (pr.kb * kBKe) + c.kblk * kBKe;
 #pragma unroll
         for (int h = 0; h < kElem; ++h)
-          tma_load_2d(dst + h * (kUnitBytes / kElem), tm, pc.tile * 128 + h * kBKe, y, &t.full_a[s]);
+          tma_load_2d_hint(dst + h * (kUnitBytes / kElem), tm, c.tile * 128 + h * kBKe, y, &t.full_a[s], policy);
       } else {
-        tma_load_2d(dst, tm, pc.kblk * kBKe, e * (pr.tiles * 128) + pc.tile * 128, &t.full_a[s]);
+        tma_load_2d_hint(dst, tm, c.kblk * kBKe, e * (pr.tiles * 128) + c.tile * 128, &t.full_a[s], policy);
       }
-      pc.next(pr);
+      it += kProdWarps;
+      if (it >= stop) return;
+      c.next(pr, kProdWarps);
     }
   };
 
   for (int ph = 0; ph < 2; ++ph) {
-    const Product &pr = prod[ph];
-    const int end = ph ? n1 + n2 : n1;
-    if (warp == 0) {
-      // the second product's first stages are started before the barriers
-      if (lane == 0) produce(ph ? end : min(n1 + kSt, n1 + n2));
-      __syncwarp();
-    } else if (warp == 1) {
+    const Product pr = ph ? prod2 : prod1;
+    const int begin = ph ? n1 : 0, end = begin + pr.n;
+    if (warp < kProdWarps) {
       if (lane == 0) {
-        Cursor c;
-        if (it < end) c.seek(pr, pr.lo);
-        for (; ok && it < end; ++it, c.next(pr)) {
-          const int s = it % kSt, buf = it % kBufs;
-          if (!mbar_wait(&t.tempty[buf], ((it / kBufs) & 1) ^ 1, ctl) ||
-              !mbar_wait(&t.full_a[s], (it / kSt) & 1, ctl) || !mbar_wait(&t.full_b[s], (it / kSt) & 1, ctl)) {
+        if (ph == 0) {
+          produce(0, prod1, 0, n1);
+          // the second product's first stages are started before the barriers
+          produce(1, prod2, n1, min(n1 + kSt, n1 + n2));
+        } else {
+          produce(1, prod2, n1, n1 + n2);
+        }
+      }
+      __syncwarp();
+    } else if (warp < kMmaWarp0 + kMmaWarps) {
+      if (lane == 0) {
+        const int mw = warp - kMmaWarp0;
+        int u = begin + (mw - begin % kMmaWarps + kMmaWarps) % kMmaWarps;
+        Cursor c{};
+        if (ok && u < end) c.seek(pr, u - begin);
+        const uint64_t a_desc = kMN ? smem_desc_sw128(smem_u32(sA), kUnitBytes / kElem, 1024)
+                                    : smem_desc_sw128(smem_u32(sA), 16, 1024);
+        const uint64_t b_desc = smem_desc_sw128(smem_u32(sB), 16, 1024);
+        constexpr int kAStep = (kMN ? (32 / kElem) * 128 : 32) >> 4;  // descriptor units (16 bytes) per MMA
+        int open = -1;  // the item this issuer is summing
+        uint32_t idesc = 0, d = 0;
+        for (; ok && u < end;) {
+          const int s = u % kSt;
+          bool first = c.item != open;
+          if (first) {
+            open = c.item;
+            const int g = items + open, buf = g % kBufs;
+            idesc = instr_desc_mn(kElem == 2, kMN, false, static_cast<uint32_t>(mma_cols(t.g_count[c.group])), 128u);
+            d = tbase + (buf * kMmaWarps + mw) * kBufCols;
+            if (!mbar_wait(&t.tempty[buf], ((g / kBufs) & 1) ^ 1, ctl)) {
+              ok = false;
+              break;
+            }
+          }
+          // the loader has seen the weights land
+          if (!mbar_wait(&t.full[s], (u / kSt) & 1, ctl)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t idesc =
-              instr_desc_mn(kElem == 2, kMN, false, static_cast<uint32_t>(mma_cols(t.g_count[c.group])), 128u);
-          const uint32_t a0 = smem_u32(sA + s * kUnitBytes), b0 = smem_u32(sB + s * kBBytes);
+          const uint64_t ad = a_desc + s * (kUnitBytes >> 4), bd = b_desc + s * (kBBytes >> 4);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t ad = kMN ? smem_desc_sw128(a0 + kk * (32 / kElem) * 128, kUnitBytes / kElem, 1024)
-                                    : smem_desc_sw128(a0 + kk * 32, 16, 1024);
-            tc_mma<kElem == 2>(tbase + buf * kBufCols, ad, smem_desc_sw128(b0 + kk * 32, 16, 1024), idesc,
-                               kk ? 1u : 0u);
+            tc_mma<kElem == 2>(d, ad + kk * kAStep, bd + kk * 2, idesc, first ? 0u : 1u);
+            first = false;
           }
-          tc_commit(&t.empty[s]);
-          tc_commit(&t.tfull[buf]);
+          tc_commit(&t.done[s]);
+          if (c.kblk + kMmaWarps >= c.kend) tc_commit(&t.tfull[(items + open) % kBufs][mw]);
+          u += kMmaWarps;
+          if (u < end) c.next(pr, kMmaWarps);
         }
       }
       __syncwarp();
@@ -369,150 +502,148 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       const int lw = warp - kLoadWarp0;
       const __nv_bfloat16 *src = ph ? p.h : p.x;
       const int64_t ld = static_cast<int64_t>(pr.kb) * kBKe;
-      // lane's values of a row's block: 4 (E4M3) or 2 (bf16)
-      uint2 ahead[C::kAhead][kRowsPerWarp];
-      auto fetch = [&](const Cursor &c, uint2 (&r)[kRowsPerWarp]) {
-        const int n = t.g_count[c.group], f = t.g_first[c.group];
+      // eight rows of a unit: lane's 4 (E4M3) or 2 (bf16) values of each block
+      uint2 raw[8];
+      Cursor c{};
+      auto fetch = [&](uint2 (&r)[8], int r0) {
+        const int n = t.g_count[c.group] - r0, f = t.g_first[c.group] + r0;
+        const __nv_bfloat16 *base = src + static_cast<int64_t>(c.kblk) * kBKe + lane * (kBKe / 32);
 #pragma unroll
-        for (int i = 0; i < kRowsPerWarp; ++i) {
-          const int row = lw + kLoadWarps * i;
-          if (row < n) {
-            const int q = t.rows[f + row];
-            const __nv_bfloat16 *a =
-                src + (ph ? q : q / p.k) * ld + static_cast<int64_t>(c.kblk) * kBKe + lane * (kBKe / 32);
+        for (int i = 0; i < 8; ++i) {
+          if (i < n) {
+            const int q = t.rows[f + i];
+            const __nv_bfloat16 *a = base + (ph ? q : static_cast<int>(t.token[q])) * ld;
             if constexpr (kElem == 1) r[i] = __ldcg(reinterpret_cast<const uint2 *>(a));
             else r[i].x = __ldcg(reinterpret_cast<const uint32_t *>(a));
           }
         }
       };
-      const int n = end - it;
-      Cursor c, f;
-      if (n > 0) {
-        c.seek(pr, pr.lo);
-        f.seek(pr, pr.lo);
+      int u = begin + (lw - begin % kLoadWarps + kLoadWarps) % kLoadWarps;  // this warp's units: u % 8 == lw
+      if (u < end) {
+        c.seek(pr, u - begin);
+        fetch(raw, 0);
       }
-      int fetched = 0;
-#pragma unroll
-      for (int d = 0; d < C::kAhead; ++d)
-        if (fetched < n) {
-          fetch(f, ahead[d]);
-          f.next(pr);
-          ++fetched;
+      for (; ok && u < end; u += kLoadWarps) {
+        const int s = u % kSt;
+        bool got = mbar_wait(&t.done[s], ((u / kSt) & 1) ^ 1, ctl);
+        if (!__all_sync(0xffffffffu, got)) {
+          ok = false;
+          break;
         }
-      for (int done = 0; ok && done < n;) {
+        const int cnt = t.g_count[c.group], lo_row = (cnt + 7) & ~7, f = t.g_first[c.group];
+        uint8_t *b = sB + s * kBBytes;
+        for (int r0 = 0; r0 < kRows; r0 += 8) {
+          if (kRows > 8 && r0 >= cnt) break;
+          uint2 next[8];
+          if (kRows > 8 && r0 + 8 < cnt) fetch(next, r0 + 8);
 #pragma unroll
-        for (int d = 0; d < C::kAhead; ++d) {
-          if (done >= n || !ok) continue;
-          const int s = it % kSt, slot = it % kRing;
-          bool got = mbar_wait(&t.empty[s], ((it / kSt) & 1) ^ 1, ctl);
-          if (!__all_sync(0xffffffffu, got)) {
-            ok = false;
-            continue;
-          }
-          const int cnt = t.g_count[c.group], lo_row = (cnt + 7) & ~7;
-          uint8_t *b = sB + s * kBBytes;
-#pragma unroll
-          for (int i = 0; i < kRowsPerWarp; ++i) {
-            const int row = lw + kLoadWarps * i;
-            if (row < cnt) {
-              const uint32_t at = static_cast<uint32_t>(row * 128 + ((lane * 4) ^ ((row & 7) << 4)));
+          for (int i = 0; i < 8; ++i) {
+            if (r0 + i < cnt) {
+              const uint32_t at = static_cast<uint32_t>((r0 + i) * 128 + ((lane * 4) ^ (i << 4)));
               if constexpr (kElem == 1) {
                 uint32_t hi, lo;
-                const float inv = split_e4m3(ahead[d][i], hi, lo);
+                const int q = t.rows[f + r0 + i];
+                split_e4m3(raw[i], t.up[ph ? q : static_cast<int>(t.token[q])], hi, lo);
                 *reinterpret_cast<uint32_t *>(b + at) = hi;
                 *reinterpret_cast<uint32_t *>(b + lo_row * 128 + at) = lo;
-                if (lane == 0) t.inv_scale[slot][row] = inv;
               } else {
-                *reinterpret_cast<uint32_t *>(b + at) = ahead[d][i].x;
+                *reinterpret_cast<uint32_t *>(b + at) = raw[i].x;
               }
             }
           }
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&t.full_b[s]);
-            mbar_arrive(&t.sfull[slot]);
-          }
-          if (fetched < n) {
-            fetch(f, ahead[d]);
-            f.next(pr);
-            ++fetched;
-          }
-          c.next(pr);
-          ++done;
-          ++it;
+          if (kRows > 8)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) raw[i] = next[i];
         }
+        fence_async_smem();
+        __syncwarp();
+        // the next unit's rows are on their way while the weights land
+        if (u + kLoadWarps < end) {
+          c.next(pr, kLoadWarps);
+          fetch(raw, 0);
+        }
+        if (lane == 0 && (got = mbar_wait(&t.full_a[s], (u / kSt) & 1, ctl))) mbar_arrive(&t.full[s]);
+        ok = __shfl_sync(0xffffffffu, got ? 1 : 0, 0);
       }
     } else {
       // ---------------------------------------------------------- epilogue
       const int q4 = warp & 3;
       const uint32_t tl = tbase + (static_cast<uint32_t>(q4 * 32) << 16);
       const int64_t cols = static_cast<int64_t>(pr.tiles) * 128;
-      float acc[kRows];
-#pragma unroll
-      for (int i = 0; i < kRows; ++i) acc[i] = 0.0f;
-      Cursor c;
-      if (it < end) c.seek(pr, pr.lo);
-      for (; it < end; ++it) {
-        const int buf = it % kBufs, slot = it % kRing;
-        bool got = mbar_wait(&t.tfull[buf], (it / kBufs) & 1, ctl);
-        if (got) got = mbar_wait(&t.sfull[slot], (it / kRing) & 1, ctl);
+      // one pass per item: the issuers' sums of the whole (sliced) contraction
+      Cursor c{};
+      it = begin;
+      if (it < end) c.seek(pr, 0);
+      while (ok && it < end) {
+        const int len = c.kend - c.kblk, buf = (items + c.item) % kBufs;
+        bool got = true;
+        for (int m = 0; m < kMmaWarps; ++m) {
+          // issuer m has units of the item unless it is one unit of the other's
+          if (len > 1 || it % kMmaWarps == m) {
+            if (got) got = mbar_wait(&t.tfull[buf][m], (tphase >> (buf * kMmaWarps + m)) & 1, ctl);
+            tphase ^= 1u << (buf * kMmaWarps + m);
+          }
+        }
         if (!__all_sync(0xffffffffu, got)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const int cnt = t.g_count[c.group], lo_col = (cnt + 7) & ~7;
+        const int cnt = t.g_count[c.group], lo_col = (cnt + 7) & ~7, f = t.g_first[c.group];
+        const int in_tile = q4 * 32 + lane;
+        // slice 0 to [pair][column], the others to
+        // [slice - 1][tile left over][row][128]
+        float *dst = p.partial + c.tile * 128 + in_tile;
+        float *more = p.extra + static_cast<int64_t>((c.slice - 1) * pr.left + c.left_tile) * kRows * 128 + in_tile;
+#pragma unroll 1
+        for (int r = 0; r < cnt; r += 8) {
+          float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-        for (int r = 0; r < kRows; r += 8) {
-          if (r < cnt) {
-            uint32_t a[8];
-            tmem_ld8(tl + buf * kBufCols + r, a);
-            if constexpr (kElem == 1) {
-              uint32_t b[8];
-              tmem_ld8(tl + buf * kBufCols + lo_col + r, b);
+          for (int m = 0; m < kMmaWarps; ++m) {
+            if (len > 1 || it % kMmaWarps == m) {
+              const uint32_t at = tl + (buf * kMmaWarps + m) * kBufCols + r;
+              uint32_t a[8], b[8];
+              tmem_ld8(at, a);
+              if constexpr (kElem == 1) tmem_ld8(at + lo_col, b);
               tmem_wait_ld();
 #pragma unroll
               for (int i = 0; i < 8; ++i)
-                acc[r + i] = __fmaf_rn(__fmaf_rn(__uint_as_float(b[i]), 0.0625f, __uint_as_float(a[i])),
-                                       t.inv_scale[slot][r + i], acc[r + i]);
-            } else {
-              tmem_wait_ld();
+                v[i] += kElem == 1 ? __fmaf_rn(__uint_as_float(b[i]), 0.0625f, __uint_as_float(a[i]))
+                                   : __uint_as_float(a[i]);
+            }
+          }
 #pragma unroll
-              for (int i = 0; i < 8; ++i) acc[r + i] += __uint_as_float(a[i]);
+          for (int i = 0; i < 8; ++i) {
+            if (r + i < cnt) {
+              const int q = t.rows[f + r + i];
+              if constexpr (kElem == 1) v[i] *= inverse_of_power(t.up[ph ? q : static_cast<int>(t.token[q])]);
+              if (c.slice == 0) dst[q * cols] = v[i];
+              else more[(r + i) * 128] = v[i];
             }
           }
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&t.tempty[buf]);
-        if (c.kblk == pr.kb - 1 || it == end - 1) {
-          // this CTA's partial sum of the tile: [slot][pair][column]
-          const uint64_t u0 = (static_cast<uint64_t>(c.group) * pr.tiles + c.tile) * pr.kb;
-          const uint32_t part = blockIdx.x - pr.cta_of(u0);
-          const int f = t.g_first[c.group];
-          float *dst = p.partial + static_cast<int64_t>(part) * p.pairs * cols + c.tile * 128 + q4 * 32 + lane;
-#pragma unroll
-          for (int r = 0; r < kRows; ++r) {
-            if (r < cnt) dst[t.rows[f + r] * cols] = acc[r];
-            acc[r] = 0.0f;
-          }
-        }
-        c.next(pr);
+        it += len;
+        if (it < end) c.next(pr, len);
       }
     }
+    items += pr.items;
     grid.sync();
 
-    // sum of a tile's partials for one pair and four columns
+    // sum of a tile's slices for one pair and four columns
     const int64_t cols = static_cast<int64_t>(pr.tiles) * 128;
     auto total4 = [&](int pair, int col) -> float4 {
-      const uint64_t u0 = (static_cast<uint64_t>(t.pair_group[pair]) * pr.tiles + col / 128) * pr.kb;
-      const uint32_t parts = pr.cta_of(u0 + pr.kb - 1) - pr.cta_of(u0) + 1;
-      const float *src = p.partial + pair * cols + col;
-      float4 a = __ldcg(reinterpret_cast<const float4 *>(src));
-      for (uint32_t i = 1; i < parts; ++i) {
-        const float4 b = __ldcg(reinterpret_cast<const float4 *>(src + i * p.pairs * cols));
-        a = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+      float4 a = __ldcg(reinterpret_cast<const float4 *>(p.partial + pair * cols + col));
+      const int lt = t.pair_group[pair] * pr.tiles + col / 128 - pr.waves * static_cast<int>(gridDim.x);
+      if (lt >= 0) {
+        const float *src = p.extra + (static_cast<int64_t>(lt) * kRows + t.pos[pair] % kRows) * 128 + col % 128;
+        const int64_t step = static_cast<int64_t>(pr.left) * kRows * 128;
+        for (int i = 1; i < pr.slices; ++i) {
+          const float4 b = __ldcg(reinterpret_cast<const float4 *>(src + (i - 1) * step));
+          a = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+        }
       }
       return a;
     };
@@ -535,8 +666,20 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         __nv_bfloat162 o[2] = {__floats2bfloat162_rn(few_silu(g.x) * u.x, few_silu(g.y) * u.y),
                                __floats2bfloat162_rn(few_silu(g.z) * u.z, few_silu(g.w) * u.w)};
         *reinterpret_cast<uint2 *>(p.h + static_cast<int64_t>(pair) * F + col) = *reinterpret_cast<uint2 *>(o);
+        if constexpr (kElem == 1) {
+          // the row's largest, of the rounded values (a maximum: any order)
+          const float2 a = __bfloat1622float2(o[0]), b = __bfloat1622float2(o[1]);
+          const uint32_t m = max(max(finite_bits(a.x), finite_bits(a.y)), max(finite_bits(b.x), finite_bits(b.y)));
+          const unsigned act = __activemask(), same = __match_any_sync(act, pair);
+          const uint32_t w = __reduce_max_sync(same, m);
+          if (lane == __ffs(same) - 1) atomicMax(p.largest + p.T + pair, w);
+        }
       }
       grid.sync();
+      if constexpr (kElem == 1) {
+        for (int q = tid; q < p.pairs; q += kFewThreads) t.up[q] = row_scale_up(__ldcg(p.largest + p.T + q));
+        __syncthreads();
+      }
     } else {
       const int N = p.N;
       for (int64_t i = first; i < static_cast<int64_t>(p.T) * (N / 4); i += nthreads) {
@@ -565,18 +708,20 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   }
 
   // every copy and MMA has ended before the CTA leaves
-  if (warp == 0 && lane == 0)
-    for (int i = it > kSt ? it - kSt : 0; i < it; ++i) mbar_wait(&t.full_a[i % kSt], (i / kSt) & 1, ctl_drain);
-  if (warp == 1) {
+  if (warp >= kMmaWarp0 && warp < kMmaWarp0 + kMmaWarps) {
     if (lane == 0) {
-      tc_commit(&t.drain);
-      mbar_wait(&t.drain, 0, ctl_drain);
+      tc_commit(&t.drain[warp - kMmaWarp0]);
+      mbar_wait(&t.drain[warp - kMmaWarp0], 0, ctl_drain);
     }
     __syncwarp();
   }
+  __syncthreads();
+  if (tid == 0)
+    for (int s = 0; s < kSt; ++s)
+      if (t.last[s] >= 0) mbar_wait(&t.full_a[s], (t.last[s] / kSt) & 1, ctl_drain);
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == kMmaWarp0) {
     tc_fence_after();
     tmem_dealloc(tbase, kTmem);
   }
@@ -589,8 +734,11 @@ cudaError_t launch_few_inst(const CUtensorMap &tm1, const CUtensorMap &tm2, cons
   static_assert(smem <= 232448, "shared memory of one CTA");
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
+  // no more CTAs than units: the barriers of a small layer span fewer SMs
+  const int64_t units = static_cast<int64_t>(p.pairs) * max(p.tiles1 * p.kb1, p.tiles2 * p.kb2);
+  const int grid = static_cast<int>(units < num_sms() ? units : num_sms());
   void *args[] = {const_cast<CUtensorMap *>(&tm1), const_cast<CUtensorMap *>(&tm2), const_cast<FewParams *>(&p)};
-  return cudaLaunchCooperativeKernel(reinterpret_cast<const void *>(kern), dim3(num_sms()), dim3(kFewThreads), args,
+  return cudaLaunchCooperativeKernel(reinterpret_cast<const void *>(kern), dim3(grid), dim3(kFewThreads), args,
                                      smem, st);
 }
 
@@ -602,13 +750,9 @@ cudaError_t launch_few_rows(const CUtensorMap &tm1, const CUtensorMap &tm2, cons
 
 }  // namespace
 
-int few_parts(int64_t tiles, int64_t kb) {
-  // fewest units: one group.  A CTA's range then holds at least `len` units,
-  // so a tile's kb units lie in at most (kb - 1) / len + 2 ranges
-  const int64_t len = tiles * kb / num_sms();
-  if (len == 0) return static_cast<int>(kb);
-  const int64_t parts = (kb - 1) / len + 2;
-  return static_cast<int>(parts < kb ? parts : kb);
+size_t few_extra_floats(int64_t T) {
+  // tiles left over (fewer than CTAs) x (slices - 1) x rows of a group x 128
+  return static_cast<size_t>(num_sms()) * (kFewMaxSlices - 1) * (T <= 8 ? 8 : 32) * 128;
 }
 
 cudaError_t launch_moe_few(int elem, bool mn_major, const CUtensorMap &tm1, const CUtensorMap &tm2,

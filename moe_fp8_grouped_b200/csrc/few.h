@@ -17,7 +17,9 @@ struct FewParams {
   const float *weights;    // [T, k]
   const float *s1, *s2;    // [G, 2F], [G, N] (E4M3 weights)
   __nv_bfloat16 *h;        // [pairs, F] silu(gate) * up
-  float *partial;          // [parts][pairs][columns] partial sums of a product
+  uint32_t *largest;       // [T] and [pairs]: largest magnitudes of the rows of x and h (fp32 bits)
+  float *partial;          // [pairs][columns] sums of a product (its tiles' first slice)
+  float *extra;            // few_extra_floats: the other slices of tiles left over
   void *y;                 // [T, N]
   int T, k, pairs, G, F, N;
   int tiles1, kb1, tiles2, kb2;  // 128-column tiles and contraction blocks of the two products
@@ -26,8 +28,8 @@ struct FewParams {
   uint64_t wait_limit_ns;
 };
 
-// Partial sums a 128-column tile with kb contraction blocks can get at most.
-int few_parts(int64_t tiles, int64_t kb);
+// Floats of FewParams::extra for T tokens.
+size_t few_extra_floats(int64_t T);
 
 cudaError_t launch_moe_few(int elem, bool mn_major, const CUtensorMap &tm1, const CUtensorMap &tm2,
                            const FewParams &p, cudaStream_t st);

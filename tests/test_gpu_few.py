@@ -13,6 +13,7 @@ import torch
 
 import moe_fp8_grouped_b200 as gm
 import oracle
+from moe_fp8_grouped_b200 import _binding as B
 from moe_fp8_grouped_b200 import ep
 from parity import TOL, assert_within, check_guards, guarded
 
@@ -133,7 +134,7 @@ def test_no_token_has_an_expert():
 def test_activation_magnitudes():
     """Rows of very different size, outliers within a block, zeros, bf16
     subnormals and the largest values: the E4M3 pair keeps each value to 2^-22
-    of its block's largest, below the 2e-3 * A of the bound."""
+    of its row's largest, below the 2e-3 * A of the bound."""
     T, k, G, K, F, N = 8, 1, 2, 512, 128, 256
     w, d1, d2 = _layer(G, K, F, N, "e4m3", False)
     x, ids, wts = _inputs(T, k, G, K, seed=5)
@@ -243,7 +244,8 @@ def test_agrees_with_the_routed_products():
 def test_device_status_is_clean():
     w, _, _ = _layer(4, 256, 128, 256, "e4m3", False)
     x, ids, wts = _inputs(4, 2, 4, 256, seed=2)
-    ws = torch.full((1 << 20,), 0xFF, dtype=torch.uint8, device=DEV)  # contents do not matter
+    need = B.lib().gmm_moe_few_workspace_bytes(4, 2, 4, 256, 128, 256, B.DT_E4M3)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device=DEV)  # contents do not matter
     y = gm.gmm_moe_few(x, ids, wts, *w, ws=ws)
     assert gm.gmm_read_device_status(ws) == (0, 0)
     assert torch.equal(y, gm.gmm_moe_few(x, ids, wts, *w))
