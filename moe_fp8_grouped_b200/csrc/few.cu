@@ -62,7 +62,7 @@ namespace {
 
 constexpr int kFewThreads = 512;
 constexpr int kFewMaxSlices = 16;
-constexpr int kFewOwnTokens = 30;  // rows whose largest value every CTA finds on its own
+constexpr int kFewOwnTokens = 4;   // rows whose largest value every CTA finds on its own
 constexpr int kUnitBytes = 16384;  // 128 columns x 128 bytes of contraction
 constexpr int kProdWarps = 2;                // warps 0 .. 1
 constexpr int kMmaWarp0 = 2, kMmaWarps = 2;
@@ -84,19 +84,105 @@ struct FewCfg<32> {
 template <int kRows>
 constexpr int few_b_bytes() { return 2 * kRows * 128; }  // hi rows and lo rows
 
+// a / b for 0 <= a < 2^24, b > 0: the set-up and the tile switches divide by
+// sizes known only at run time, and the code of exact integer divisions cost
+// more (cold instruction fetches) than they compute
+__device__ __forceinline__ int few_div(int a, int b) {
+  int q = static_cast<int>(__fdividef(static_cast<float>(a), static_cast<float>(b)));  // off by one at most
+  const int r = a - q * b;
+  q += r >= b ? 1 : 0;
+  return r < 0 ? q - 1 : q;
+}
+
+// One of the two products: `tiles` column tiles per group, kb contraction
+// blocks.  The tiles of all groups are numbered; the first waves * gridDim.x go
+// whole to CTA (number % gridDim.x), the `left` others as `slices` slices of
+// their contraction, item (slice, tile) to CTA (item number % gridDim.x).
+struct Product {
+  int tiles, kb, waves, left, slices;
+  int n, items;  // this CTA's units, and the items (tiles or slices) they belong to
+  // by one warp, all lanes with the same result
+  __device__ __forceinline__ void plan(int ngroups, int tiles_, int kb_, int lane) {
+    tiles = tiles_;
+    kb = kb_;
+    const int grid = gridDim.x, total = ngroups * tiles;
+    waves = few_div(total, grid);
+    left = total - waves * grid;
+    // slices that make the CTA with the most units have the fewest (of those
+    // the smallest count): one candidate per lane
+    const int c = min(lane + 1, kFewMaxSlices);
+    unsigned cost = static_cast<unsigned>(few_div(left * c + grid - 1, grid)) * few_div(kb + c - 1, c) * 32u + c;
+    if (c > kb) cost = 0xffffffffu;
+    slices = static_cast<int>(__reduce_min_sync(0xffffffffu, cost) & 31u);
+    // the CTA's slice items, one per lane (at most 16: left < grid)
+    const int j = lane * grid + blockIdx.x;
+    int len = 0;
+    if (j < left * slices) {
+      const int i = few_div(j, left);
+      len = slice_begin(i + 1) - slice_begin(i);
+    }
+    n = waves * kb + __reduce_add_sync(0xffffffffu, len);
+    items = waves + __popc(__ballot_sync(0xffffffffu, len > 0));
+  }
+  __device__ __forceinline__ int slice_begin(int i) const { return few_div(i * kb, slices); }
+};
+
+// Position in this CTA's units of a product.
+struct Cursor {
+  int item;              // waves first, then the CTA's slice items
+  int group, tile;       // column tile `tile` of group `group`
+  int kblk, kend;        // contraction block, end of the item's
+  int left_tile, slice;  // number among the tiles left over (-1: a whole tile)
+  __device__ __forceinline__ void open(const Product &p) {
+    int gt = item * gridDim.x + blockIdx.x, k0 = 0;
+    kend = p.kb;
+    slice = 0;
+    left_tile = -1;
+    if (item >= p.waves) {
+      const int j = gt - p.waves * gridDim.x;
+      slice = few_div(j, p.left);
+      left_tile = j - slice * p.left;
+      gt = p.waves * gridDim.x + left_tile;
+      k0 = p.slice_begin(slice);
+      kend = p.slice_begin(slice + 1);
+    }
+    group = few_div(gt, p.tiles);
+    tile = gt - group * p.tiles;
+    kblk += k0;
+  }
+  __device__ __forceinline__ void next(const Product &p, int by = 1) {
+    kblk += by;
+    while (kblk >= kend) {
+      kblk -= kend;
+      ++item;
+      open(p);
+    }
+  }
+  // to unit `u` of the CTA (u < p.n)
+  __device__ __forceinline__ void seek(const Product &p, int u) {
+    item = -1;
+    kend = 0;
+    kblk = u;
+    next(p, 0);
+  }
+};
+
 // shared memory behind the stages
 template <int kRows>
 struct FewTail {
   using C = FewCfg<kRows>;
   // stage s: weights landed; weights landed and rows written; MMAs done
   uint64_t full_a[C::kStages], full[C::kStages], done[C::kStages];
-  // accumulator b: sums of issuer i complete; read
-  uint64_t tfull[C::kBufs][kMmaWarps], tempty[C::kBufs];
+  // accumulator b: sums of issuer i complete
+  uint64_t tfull[C::kBufs][kMmaWarps];
   uint64_t drain[kMmaWarps];
-  int last[C::kStages];  // the stage's newest copy (unit), -1: none
+  uint64_t tempty[C::kBufs];  // accumulator b: read (the only barrier with more than one arrival)
+  int last[C::kStages];       // the stage's newest copy (unit), -1: none
   uint32_t tmem_slot;
-  int abort_flag, no_abort, ngroups;
-  int slices[2];  // of each product's tiles left over
+  int abort_flag, no_abort;
+  Product prod[2];
+  int scan[kFewThreads / 32];        // rows and groups of each warp's experts
+  uint32_t big[kFewOwnTokens];       // largest magnitude of each token's row (bf16 bits)
   float up[kFewMaxPairs];            // power of two that scales each pair's row (E4M3)
   int cnt[kMaxGroups];               // rows per expert, then group offset
   uint16_t first[kMaxGroups];        // first entry of the expert in rows[]
@@ -114,84 +200,6 @@ constexpr size_t few_smem_bytes() {
          sizeof(FewTail<kRows>);
 }
 
-// One of the two products: `tiles` column tiles per group, kb contraction
-// blocks.  The tiles of all groups are numbered; the first waves * gridDim.x go
-// whole to CTA (number % gridDim.x), the `left` others as `slices` slices of
-// their contraction, item (slice, tile) to CTA (item number % gridDim.x).
-struct Product {
-  int tiles, kb, waves, left, slices;
-  int n, items;  // this CTA's units, and the items (tiles or slices) they belong to
-  __device__ __forceinline__ void init(int ngroups, int tiles_, int kb_) {
-    tiles = tiles_;
-    kb = kb_;
-    const int grid = gridDim.x, total = ngroups * tiles;
-    waves = total / grid;
-    left = total - waves * grid;
-  }
-  // slices that make the CTA with the most units have the fewest (of those the
-  // smallest count): one candidate per lane, the first 16 lanes
-  __device__ __forceinline__ int best_slices(int lane) const {
-    const int c = lane + 1, grid = gridDim.x;
-    unsigned cost = 0xffffffffu;
-    if (c <= kFewMaxSlices && c <= kb)
-      cost = static_cast<unsigned>((left * c + grid - 1) / grid) * ((kb + c - 1) / c) * 32u + c;
-    return static_cast<int>(__reduce_min_sync(0xffffffffu, cost) & 31u);
-  }
-  __device__ __forceinline__ int slice_begin(int i) const { return i * kb / slices; }
-  __device__ __forceinline__ void count(int slices_) {
-    slices = slices_;
-    n = waves * kb;
-    items = waves;
-    for (int j = blockIdx.x; j < left * slices; j += gridDim.x) {
-      const int i = j / left;
-      n += slice_begin(i + 1) - slice_begin(i);
-      ++items;
-    }
-  }
-};
-
-// Position in this CTA's units of a product.
-struct Cursor {
-  int item;              // waves first, then the CTA's slice items
-  int group, tile;       // column tile `tile` of group `group`
-  int kblk, kend;        // contraction block, end of the item's
-  int left_tile, slice;  // number among the tiles left over (-1: a whole tile)
-  __device__ __forceinline__ void open(const Product &p) {
-    int gt, k0 = 0;
-    kend = p.kb;
-    slice = 0;
-    left_tile = -1;
-    if (item < p.waves) {
-      gt = item * gridDim.x + blockIdx.x;
-    } else {
-      const int j = (item - p.waves) * gridDim.x + blockIdx.x;
-      slice = j / p.left;
-      left_tile = j - slice * p.left;
-      gt = p.waves * gridDim.x + left_tile;
-      k0 = p.slice_begin(slice);
-      kend = p.slice_begin(slice + 1);
-    }
-    group = gt / p.tiles;
-    tile = gt - group * p.tiles;
-    kblk += k0;
-  }
-  // to unit `u` of the CTA (u < p.n)
-  __device__ __forceinline__ void seek(const Product &p, int u) {
-    item = 0;
-    kblk = 0;
-    open(p);
-    if (u) next(p, u);
-  }
-  __device__ __forceinline__ void next(const Product &p, int by = 1) {
-    kblk += by;
-    while (kblk >= kend) {
-      kblk -= kend;
-      ++item;
-      open(p);
-    }
-  }
-};
-
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&v)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
@@ -206,10 +214,11 @@ __device__ __forceinline__ float2 e4m3x2_to_f32(uint16_t c) {
   return __half22float2(*reinterpret_cast<__half2 *>(&h));
 }
 
-// Power of two that puts a row's largest finite magnitude (as fp32 bits) into
-// [128, 256); at most 2^126, so that its inverse stays normal.
+// Power of two that puts a row's largest magnitude (bf16 bits) into [128, 256);
+// at most 2^126, so that its inverse stays normal.  1 for a row with a value
+// that is not finite (its results are NaN whatever the scale).
 __device__ __forceinline__ float row_scale_up(uint32_t largest) {
-  const int e = largest == 0 ? 0 : min(134 - static_cast<int>(largest >> 23), 126);
+  const int e = largest == 0 || largest >= 0x7f80u ? 0 : min(134 - static_cast<int>(largest >> 7), 126);
   return __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 }
 
@@ -217,11 +226,8 @@ __device__ __forceinline__ float inverse_of_power(float up) {
   return __uint_as_float(0x7f000000u - __float_as_uint(up));  // 2^-e of 2^e
 }
 
-// |x| as fp32 bits, 0 when x is not finite
-__device__ __forceinline__ uint32_t finite_bits(float x) {
-  const uint32_t a = __float_as_uint(x) & 0x7fffffffu;
-  return a >= 0x7f800000u ? 0u : a;
-}
+// the larger magnitudes of two pairs of bf16 values (as bits)
+__device__ __forceinline__ uint32_t max_abs2(uint32_t m, uint32_t v) { return __vmaxu2(m, v & 0x7fff7fffu); }
 
 // Four bf16 values, scaled, as E4M3 hi and lo codes.  A value that is not
 // finite becomes NaN.
@@ -271,25 +277,20 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   }
   for (int i = tid; i < p.G; i += kFewThreads) t.cnt[i] = 0;
   if (kElem == 1 && blockIdx.x == 0)
-    for (int i = tid; i < p.pairs; i += kFewThreads) p.largest[p.T + i] = 0;  // of h, for the barrier after the first product
+    for (int i = tid; i < p.pairs; i += kFewThreads) p.largest[p.T + i] = 0;  // of h, set after the first product
+  constexpr int kBars = 3 * kSt + kBufs * kMmaWarps + kMmaWarps;
+  if (tid < kBars + kBufs) mbar_init(&t.full_a[0] + tid, tid < kBars ? 1 : kFewEpiWarps);
+  if (tid < kSt) t.last[tid] = -1;
+  if (tid < kFewOwnTokens) t.big[tid] = 0;
   if (tid == 0) {
-    for (int i = 0; i < kSt; ++i) {
-      t.last[i] = -1;
-      mbar_init(&t.full_a[i], 1);
-      mbar_init(&t.full[i], 1);
-      mbar_init(&t.done[i], 1);
-    }
-    for (int i = 0; i < kBufs; ++i) {
-      for (int m = 0; m < kMmaWarps; ++m) mbar_init(&t.tfull[i][m], 1);
-      mbar_init(&t.tempty[i], kFewEpiWarps);
-    }
-    for (int i = 0; i < kMmaWarps; ++i) mbar_init(&t.drain[i], 1);
     t.abort_flag = 0;
     t.no_abort = 0;
-    fence_barrier_init();
+    if (blockIdx.x == 0) *p.status = 0;
+  }
+  fence_barrier_init();
+  if (warp == 1 && lane == 0) {
     tma_prefetch_desc(&tm1);
     tma_prefetch_desc(&tm2);
-    if (blockIdx.x == 0) *p.status = 0;
   }
   if (warp == kMmaWarp0) {
     tmem_alloc(&t.tmem_slot, kTmem);
@@ -299,31 +300,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = t.tmem_slot;
-  // largest magnitude of each token's row: every CTA on its own for few tokens,
-  // shared through memory and one more barrier for many
+  // largest magnitude of each token's row: in every CTA for a few tokens, shared
+  // through memory and one more barrier for more
   const bool share = kElem == 1 && p.T > kFewOwnTokens;
-  if (kElem == 1) {
-    const int step = share ? gridDim.x * 15 : 15;
-    for (int tok = share ? blockIdx.x * 15 + warp - 1 : warp - 1; warp > 0 && tok < p.T; tok += step) {
-      const uint4 *row = reinterpret_cast<const uint4 *>(p.x + static_cast<int64_t>(tok) * (p.kb1 * kBKe));
-      uint32_t m = 0;
-#pragma unroll 8
-      for (int i = lane; i < p.kb1 * kBKe / 8; i += 32) {
-        const uint4 v = row[i];
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          m = max(m, finite_bits(__uint_as_float(w[e] << 16)));
-          m = max(m, finite_bits(__uint_as_float(w[e] & 0xffff0000u)));
-        }
-      }
-      m = __reduce_max_sync(0xffffffffu, m);
-      if (lane == 0) {
-        if (share) p.largest[tok] = m;
-        else t.up[tok] = row_scale_up(m);
-      }
-    }
-  }
   if (warp == 0) {
     // rank of every pair within its expert, in pair order
     for (int base = 0; base < p.pairs; base += 32) {
@@ -338,41 +317,74 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       if (valid && before == 0) t.cnt[id] = c + __popc(same);
       __syncwarp();
     }
-    // rows and groups of the experts, in expert order
-    int row0 = 0, grp0 = 0;
-    for (int base = 0; base < p.G; base += 32) {
-      const int e = base + lane;
-      const int c = e < p.G ? t.cnt[e] : 0;
-      const int n = (c + kRows - 1) / kRows;
-      int both = c | (n << 16);  // both prefixes in one scan (each below 2^15)
+  } else if (kElem == 1) {
+    // one warp per piece of 1024 values of a token's row (shared: per row)
+    const int pieces = (p.kb1 * 128 + 1023) >> 10, span = share ? pieces : 1;
+    const int w0 = share ? blockIdx.x * 15 + warp - 1 : warp - 1, step = share ? gridDim.x * 15 : 15;
+    for (int i = w0; i < (share ? p.T : p.T * pieces); i += step) {
+      const int tok = share ? i : few_div(i, pieces), first = share ? 0 : i - tok * pieces;
+      const __nv_bfloat16 *row = p.x + static_cast<int64_t>(tok) * (p.kb1 * 128);
+      uint32_t m = 0;
+      for (int at = first * 1024; at < (first + span) * 1024; at += 1024) {
+        uint4 v[4];
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, both, d);
-        if (lane >= d) both += o;
+        for (int e = 0; e < 4; ++e) {
+          const int c = at + (e * 32 + lane) * 8;
+          v[e] = c < p.kb1 * 128 ? *reinterpret_cast<const uint4 *>(row + c) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          m = max_abs2(max_abs2(max_abs2(max_abs2(m, v[e].x), v[e].y), v[e].z), v[e].w);
       }
-      const int last = __shfl_sync(0xffffffffu, both, 31);
-      const int r = row0 + (both & 0xffff) - c, g = grp0 + (both >> 16) - n;
-      if (e < p.G) {
-        t.first[e] = static_cast<uint16_t>(r);
-        t.cnt[e] = g;
+      m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+      if (lane == 0) {
+        if (share) p.largest[tok] = m;
+        else atomicMax(&t.big[tok], m);
       }
-      for (int i = 0; i < n; ++i) {
-        t.g_expert[g + i] = static_cast<uint16_t>(e);
-        t.g_first[g + i] = static_cast<uint16_t>(r + i * kRows);
-        t.g_count[g + i] = static_cast<uint16_t>(min(kRows, c - i * kRows));
-      }
-      row0 += last & 0xffff;
-      grp0 += last >> 16;
     }
-    Product a, b;
-    a.init(grp0, p.tiles1, p.kb1);
-    b.init(grp0, p.tiles2, p.kb2);
-    const int sa = a.best_slices(lane), sb = b.best_slices(lane);
-    if (lane == 0) {
-      t.ngroups = grp0;
-      t.slices[0] = sa;
-      t.slices[1] = sb;
+  }
+  __syncthreads();
+  // rows and groups of the experts, in expert order: two experts a thread
+  int c[2], n[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    c[i] = 2 * tid + i < p.G ? t.cnt[2 * tid + i] : 0;
+    n[i] = (c[i] + kRows - 1) / kRows;
+  }
+  const int own = (c[0] + c[1]) | ((n[0] + n[1]) << 16);  // both sums in one word (each below 2^15)
+  int upto = own;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, upto, d);
+    if (lane >= d) upto += o;
+  }
+  if (lane == 31) t.scan[warp] = upto;
+  if (kElem == 1 && !share && tid < p.T) t.up[tid] = row_scale_up(t.big[tid]);
+  __syncthreads();
+  const int other = lane < kFewThreads / 32 ? t.scan[lane] : 0;
+  const int before = __reduce_add_sync(0xffffffffu, lane < warp ? other : 0) + upto - own;
+  const int ngroups = __reduce_add_sync(0xffffffffu, other) >> 16;
+  if (own) {
+    int r = before & 0xffff, g = before >> 16;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int e = 2 * tid + i;
+      if (!c[i]) continue;
+      t.first[e] = static_cast<uint16_t>(r);
+      t.cnt[e] = g;
+      for (int k = 0; k < n[i]; ++k, ++g) {
+        t.g_expert[g] = static_cast<uint16_t>(e);
+        t.g_first[g] = static_cast<uint16_t>(r + k * kRows);
+        t.g_count[g] = static_cast<uint16_t>(min(kRows, c[i] - k * kRows));
+      }
+      r += c[i];
     }
+  }
+  if (warp == kFewThreads / 32 - 1 || warp == kFewThreads / 32 - 2) {
+    const int ph = warp & 1;
+    Product a;
+    a.plan(ngroups, ph ? p.tiles2 : p.tiles1, ph ? p.kb2 : p.kb1, lane);
+    if (lane == 0) t.prod[ph] = a;
   }
   __syncthreads();
   for (int q = tid; q < p.pairs; q += kFewThreads) {
@@ -382,21 +394,17 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     t.pair_group[q] = static_cast<int16_t>(valid ? t.cnt[id] + t.pos[q] / kRows : -1);
   }
   __syncthreads();
-
-  if (share) grid.sync();
   if (share) {
+    grid.sync();
     for (int i = tid; i < p.T; i += kFewThreads) t.up[i] = row_scale_up(__ldcg(p.largest + i));
     __syncthreads();
   }
+
   const WaitCtl ctl{p.wait_limit_ns, &t.abort_flag, p.status};
   const WaitCtl ctl_drain{p.wait_limit_ns, &t.no_abort, p.status};
-  Product prod1, prod2;
-  prod1.init(t.ngroups, p.tiles1, p.kb1);
-  prod2.init(t.ngroups, p.tiles2, p.kb2);
-  prod1.count(t.slices[0]);
-  prod2.count(t.slices[1]);
+  const Product prod1 = t.prod[0], prod2 = t.prod[1];
   const int n1 = prod1.n, n2 = prod2.n;
-  // products with block scales (E4M3) use hi and lo columns, bf16 one column a row
+  // E4M3 weights use hi and lo columns, bf16 one column a row
   auto mma_cols = [&](int count) { return kElem == 1 ? 2 * ((count + 7) & ~7) : ((count + 15) & ~15); };
 
   // Units are numbered over both products: 0 .. n1 - 1 of the first, n1 ..
@@ -632,14 +640,16 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     items += pr.items;
     grid.sync();
 
-    // sum of a tile's slices for one pair and four columns
+    // one warp sums the slices of 128 columns (a tile) of one pair, four
+    // columns a lane
     const int64_t cols = static_cast<int64_t>(pr.tiles) * 128;
-    auto total4 = [&](int pair, int col) -> float4 {
-      float4 a = __ldcg(reinterpret_cast<const float4 *>(p.partial + pair * cols + col));
-      const int lt = t.pair_group[pair] * pr.tiles + col / 128 - pr.waves * static_cast<int>(gridDim.x);
+    auto tile4 = [&](int pair, int tile) -> float4 {
+      float4 a = __ldcg(reinterpret_cast<const float4 *>(p.partial + pair * cols + tile * 128) + lane);
+      const int lt = t.pair_group[pair] * pr.tiles + tile - pr.waves * static_cast<int>(gridDim.x);
       if (lt >= 0) {
-        const float *src = p.extra + (static_cast<int64_t>(lt) * kRows + t.pos[pair] % kRows) * 128 + col % 128;
+        const float *src = p.extra + (static_cast<int64_t>(lt) * kRows + t.pos[pair] % kRows) * 128 + lane * 4;
         const int64_t step = static_cast<int64_t>(pr.left) * kRows * 128;
+#pragma unroll 4
         for (int i = 1; i < pr.slices; ++i) {
           const float4 b = __ldcg(reinterpret_cast<const float4 *>(src + (i - 1) * step));
           a = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
@@ -647,32 +657,29 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       }
       return a;
     };
-    const int64_t nthreads = static_cast<int64_t>(gridDim.x) * kFewThreads;
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * kFewThreads + tid;
+    const int nwarps = gridDim.x * (kFewThreads / 32), w0 = warp * gridDim.x + blockIdx.x;
     if (ph == 0) {
-      const int F = p.F;
-      for (int64_t i = first; i < static_cast<int64_t>(p.pairs) * (F / 4); i += nthreads) {
-        const int pair = static_cast<int>(i / (F / 4)), col = static_cast<int>(i % (F / 4)) * 4;
-        const int id = t.ids[pair];
+      const int F = p.F, ft = F / 128;
+      for (int i = w0; i < p.pairs * ft; i += nwarps) {
+        const int pair = few_div(i, ft), tile = i - pair * ft, col = tile * 128 + lane * 4;
         if (t.pair_group[pair] < 0) continue;
-        float4 g = total4(pair, col), u = total4(pair, F + col);
+        float4 g = tile4(pair, tile), u = tile4(pair, ft + tile);
         if constexpr (kElem == 1) {
-          const float *sc = p.s1 + static_cast<int64_t>(id) * 2 * F + col;
+          const float *sc = p.s1 + static_cast<int64_t>(t.ids[pair]) * 2 * F + col;
           const float4 sg = *reinterpret_cast<const float4 *>(sc), su = *reinterpret_cast<const float4 *>(sc + F);
           g = make_float4(g.x * sg.x, g.y * sg.y, g.z * sg.z, g.w * sg.w);
           u = make_float4(u.x * su.x, u.y * su.y, u.z * su.z, u.w * su.w);
         }
         // one rounding to bf16: the down product's operand type
-        __nv_bfloat162 o[2] = {__floats2bfloat162_rn(few_silu(g.x) * u.x, few_silu(g.y) * u.y),
-                               __floats2bfloat162_rn(few_silu(g.z) * u.z, few_silu(g.w) * u.w)};
-        *reinterpret_cast<uint2 *>(p.h + static_cast<int64_t>(pair) * F + col) = *reinterpret_cast<uint2 *>(o);
+        const __nv_bfloat162 o[2] = {__floats2bfloat162_rn(few_silu(g.x) * u.x, few_silu(g.y) * u.y),
+                                     __floats2bfloat162_rn(few_silu(g.z) * u.z, few_silu(g.w) * u.w)};
+        const uint2 v = *reinterpret_cast<const uint2 *>(o);
+        *reinterpret_cast<uint2 *>(p.h + static_cast<int64_t>(pair) * F + col) = v;
         if constexpr (kElem == 1) {
           // the row's largest, of the rounded values (a maximum: any order)
-          const float2 a = __bfloat1622float2(o[0]), b = __bfloat1622float2(o[1]);
-          const uint32_t m = max(max(finite_bits(a.x), finite_bits(a.y)), max(finite_bits(b.x), finite_bits(b.y)));
-          const unsigned act = __activemask(), same = __match_any_sync(act, pair);
-          const uint32_t w = __reduce_max_sync(same, m);
-          if (lane == __ffs(same) - 1) atomicMax(p.largest + p.T + pair, w);
+          uint32_t m = max_abs2(v.x & 0x7fff7fffu, v.y);
+          m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+          if (lane == 0) atomicMax(p.largest + p.T + pair, m);
         }
       }
       grid.sync();
@@ -681,14 +688,15 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         __syncthreads();
       }
     } else {
-      const int N = p.N;
-      for (int64_t i = first; i < static_cast<int64_t>(p.T) * (N / 4); i += nthreads) {
-        const int tok = static_cast<int>(i / (N / 4)), col = static_cast<int>(i % (N / 4)) * 4;
+      const int N = p.N, nt = N / 128;
+      for (int i = w0; i < p.T * nt; i += nwarps) {
+        const int tok = few_div(i, nt), tile = i - tok * nt, col = tile * 128 + lane * 4;
         float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 2
         for (int j = 0; j < p.k; ++j) {
           const int pair = tok * p.k + j;
           if (t.pair_group[pair] < 0) continue;
-          float4 v = total4(pair, col);
+          float4 v = tile4(pair, tile);
           if constexpr (kElem == 1) {
             const float4 s = *reinterpret_cast<const float4 *>(p.s2 + static_cast<int64_t>(t.ids[pair]) * N + col);
             v = make_float4(v.x * s.x, v.y * s.y, v.z * s.z, v.w * s.w);
