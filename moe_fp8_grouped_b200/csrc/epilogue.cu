@@ -22,21 +22,15 @@ constexpr int kActCols = 256;  // columns of a CTA: 32 threads of 8
 constexpr int kActRowThreads = kActThreads / 32;
 constexpr int kActUnroll = 4;
 
-__device__ __forceinline__ void unpack8(const uint4 &u, float (&v)[8]) {
-  const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&u);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __bfloat1622float2(h[i]);
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
-  }
+__device__ __forceinline__ float2 bf16x2_f32(uint32_t v) {
+  return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+__device__ __forceinline__ uint4 pack8(const float2 (&v)[4]) {
   uint4 u;
   __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&u);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+  for (int i = 0; i < 4; ++i) h[i] = __float22bfloat162_rn(v[i]);
   return u;
 }
 
@@ -68,11 +62,11 @@ __global__ void __launch_bounds__(kActThreads) act_bwd_kernel(const ActBwdParams
     r1 = min(r0 + kBlk, p.M);
   }
   if (r0 >= r1) return;
-  float sum[kParts][8];
+  float2 sum[kParts][4];
 #pragma unroll
   for (int s = 0; s < kParts; ++s)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum[s][i] = 0.0f;
+    for (int i = 0; i < 4; ++i) sum[s][i] = make_float2(0.0f, 0.0f);
   const __nv_bfloat16 *dout = p.dout + col, *z = p.z + col;
   __nv_bfloat16 *dz = p.dz + col;
   if (col_ok && tail) {
@@ -96,28 +90,28 @@ __global__ void __launch_bounds__(kActThreads) act_bwd_kernel(const ActBwdParams
       for (int u = 0; u < kActUnroll; ++u) {
         const int64_t r = rb + u * kActRowThreads;
         if (r >= r1) continue;
-        float d[8], a[8];
-        unpack8(vd[u], d);
-        unpack8(vz[u][0], a);
-        float o[kParts][8];
-        if constexpr (kGated) {
-          float b[8];
-          unpack8(vz[u][1], b);
+        float2 o[kParts][4];
+        const uint32_t *dw = reinterpret_cast<const uint32_t *>(&vd[u]);
+        const uint32_t *aw = reinterpret_cast<const uint32_t *>(&vz[u][0]);
+        const uint32_t *bw = reinterpret_cast<const uint32_t *>(&vz[u][kParts - 1]);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float s = act_sigmoid(a[i]);
-            o[0][i] = d[i] * b[i] * (s * (1.0f + a[i] * (1.0f - s)));
-            o[1][i] = d[i] * (a[i] * s);
+        for (int i = 0; i < 4; ++i) {
+          const float2 d = bf16x2_f32(dw[i]), a = bf16x2_f32(aw[i]);
+          if constexpr (kGated) {
+            const float2 b = bf16x2_f32(bw[i]), s = sigmoid2(a), as = __fmul2_rn(a, s);
+            // d silu = s + a s (1 - s)
+            const float2 ds = __ffma2_rn(as, __ffma2_rn(s, splat(-1.0f), splat(1.0f)), s);
+            o[0][i] = __fmul2_rn(__fmul2_rn(d, b), ds);
+            o[kParts - 1][i] = __fmul2_rn(d, as);
+          } else {
+            o[0][i] = __fmul2_rn(d, slope2<kAct>(a));
           }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) o[0][i] = d[i] * act_slope(kAct, a[i]);
         }
 #pragma unroll
         for (int s = 0; s < kParts; ++s) {
           __stcs(reinterpret_cast<uint4 *>(dz + r * p.N + s * p.F), pack8(o[s]));
 #pragma unroll
-          for (int i = 0; i < 8; ++i) sum[s][i] += o[s][i];
+          for (int i = 0; i < 4; ++i) sum[s][i] = __fadd2_rn(sum[s][i], o[s][i]);
         }
       }
     }
@@ -126,7 +120,7 @@ __global__ void __launch_bounds__(kActThreads) act_bwd_kernel(const ActBwdParams
 #pragma unroll
   for (int s = 0; s < kParts; ++s)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s_sum[ry][s][cx * 8 + i] = sum[s][i];
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<float2 *>(&s_sum[ry][s][cx * 8 + 2 * i]) = sum[s][i];
   __syncthreads();
   for (int i = threadIdx.x; i < kParts * kActCols; i += kActThreads) {
     const int s = i / kActCols, c = i % kActCols;

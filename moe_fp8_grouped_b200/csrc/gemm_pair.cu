@@ -614,6 +614,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         orow = static_cast<int64_t>(t.rt) * kBM + row;  // n
         row_ok = true;
       }
+      if constexpr (kEpi) {
+        if (row_ok) epi_prefetch(p, orow, sw ? t.ct * 128 + h * 64 : col0, sw ? 64 : kTN / 2);
+      }
       // writes 32 tile columns starting at tile column col (a multiple of 32)
       auto emit = [&](int col, const float(&o)[32]) {
         if constexpr (!kTg) {
@@ -714,7 +717,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (b + 1 < t.nblocks) release_slot(slot);  // the last slot is read again below
         }
         if (!ok) break;
-        if (row_ok) {
+        if constexpr (kEpi) {
+          if (row_ok)
+            epi_tile<kCh>(p, t.g, orow, t.ct, h, sw, acc, s_scol + slot * kBN, p.col_scale != nullptr, 1.0f,
+                        (kBlkScales && p.static_scale) ? s_eff : 1.0f, out_v8);
+        } else if (row_ok) {
           // per-channel rhs column scale (in every unit's slot); static lhs: s
           const float fin = ((kTg || kBlkScales) && p.static_scale) ? s_eff : 1.0f;
           const bool colmul = !kTg && p.col_scale != nullptr;
@@ -723,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               const float *fg = cf + colt(c), *fu = cf + colt(c + 2);
-              float o[32], ov[kEpi ? 32 : 1];
+              float o[32];
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
                 const float2 a = acc[c * 16 + i], b2 = acc[((c + 2) % kCh) * 16 + i];
@@ -731,17 +738,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float g1 = (colmul ? a.y * fg[2 * i + 1] : a.y) * fin;
                 const float u0 = (colmul ? b2.x * fu[2 * i] : b2.x) * fin;
                 const float u1 = (colmul ? b2.y * fu[2 * i + 1] : b2.y) * fin;
-                if constexpr (kEpi) {
-                  o[2 * i] = g0;
-                  o[2 * i + 1] = g1;
-                  ov[2 * i] = u0;
-                  ov[2 * i + 1] = u1;
-                } else {
-                  o[2 * i] = silu(g0) * u0;
-                  o[2 * i + 1] = silu(g1) * u1;
-                }
+                o[2 * i] = silu(g0) * u0;
+                o[2 * i + 1] = silu(g1) * u1;
               }
-              if constexpr (kEpi) epi_swiglu(p, t.g, orow, t.ct * 128 + h * 64 + c * 32, o, ov);
               emit(t.ct * 128 + h * 64 + c * 32, o);
             }
           } else {
@@ -760,7 +759,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 o[2 * i] = a.x * fin;
                 o[2 * i + 1] = a.y * fin;
               }
-              if constexpr (kEpi) epi_apply(p, t.g, orow, col, o);
               emit(col, o);
             }
           }
@@ -800,30 +798,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (two) release_unit(1);
         ++n0;
         if (two) ++n1;
-        if (row_ok) {
+        if constexpr (kEpi) {
+          if (row_ok)
+            epi_tile<4>(p, t.g, orow, t.ct, h, sw, acc, s_scol + slot * kBN, need_col,
+                        p.static_scale ? s_eff : 1.0f, 1.0f, out_v8);
+        } else if (row_ok) {
           const float s0 = p.static_scale ? s_eff : 1.0f;
           const float *cf = s_scol + slot * kBN;
           if (sw) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               const float *fg = cf + colt(c), *fu = cf + colt(c + 2);
-              float o[32], ov[kEpi ? 32 : 1];
+              float o[32];
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
                 const float2 a = acc[c * 16 + i], b2 = acc[(c + 2) * 16 + i];
                 const float gs0 = need_col ? fg[2 * i] : 1.0f, gs1 = need_col ? fg[2 * i + 1] : 1.0f;
                 const float us0 = need_col ? fu[2 * i] : 1.0f, us1 = need_col ? fu[2 * i + 1] : 1.0f;
-                if constexpr (kEpi) {
-                  o[2 * i] = a.x * s0 * gs0;
-                  o[2 * i + 1] = a.y * s0 * gs1;
-                  ov[2 * i] = b2.x * s0 * us0;
-                  ov[2 * i + 1] = b2.y * s0 * us1;
-                } else {
-                  o[2 * i] = silu(a.x * s0 * gs0) * (b2.x * s0 * us0);
-                  o[2 * i + 1] = silu(a.y * s0 * gs1) * (b2.y * s0 * us1);
-                }
+                o[2 * i] = silu(a.x * s0 * gs0) * (b2.x * s0 * us0);
+                o[2 * i + 1] = silu(a.y * s0 * gs1) * (b2.y * s0 * us1);
               }
-              if constexpr (kEpi) epi_swiglu(p, t.g, orow, t.ct * 128 + h * 64 + c * 32, o, ov);
               emit(t.ct * 128 + h * 64 + c * 32, o);
             }
           } else {
@@ -838,7 +832,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 o[2 * i] = a.x * s0 * (need_col ? cf[colt(c) + 2 * i] : 1.0f);
                 o[2 * i + 1] = a.y * s0 * (need_col ? cf[colt(c) + 2 * i + 1] : 1.0f);
               }
-              if constexpr (kEpi) epi_apply(p, t.g, orow, col, o);
               emit(col, o);
             }
           }
@@ -853,6 +846,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
+        if constexpr (kEpi && kElem == 2) {
+          // chunk by chunk from TMEM, in one copy of the epilogue's code
+#pragma unroll 1
+          for (int c = 0; c < (sw ? 2 : 4); ++c) {
+            uint32_t va[32], vb[32];
+            tmem_ld32(tl + buf * kTN + colt(c), va);
+            if (sw) tmem_ld32(tl + buf * kTN + colt(c + 2), vb);
+            tmem_wait_ld();
+            if (row_ok) epi_chunk(p, t.g, orow, sw, sw ? t.ct * 128 + h * 64 + c * 32 : t.ct * kTN + colt(c), va, vb, out_v8);
+          }
+        } else {
         const float s0 = p.static_scale ? s_eff : 1.0f;
         const float *cf = s_scol + slot * kBN;
 #pragma unroll
@@ -865,18 +869,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (sw) {
             if (row_ok) {
               const float *fg = cf + colt(ca), *fu = cf + colt(cb);
-              float o[32], ov[kEpi ? 32 : 1];
+              float o[32];
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
                 const float gs = need_col ? fg[i] : 1.0f, us = need_col ? fu[i] : 1.0f;
-                if constexpr (kEpi) {
-                  o[i] = __uint_as_float(va[i]) * s0 * gs;
-                  ov[i] = __uint_as_float(vb[i]) * s0 * us;
-                } else {
-                  o[i] = silu(__uint_as_float(va[i]) * s0 * gs) * (__uint_as_float(vb[i]) * s0 * us);
-                }
+                o[i] = silu(__uint_as_float(va[i]) * s0 * gs) * (__uint_as_float(vb[i]) * s0 * us);
               }
-              if constexpr (kEpi) epi_swiglu(p, t.g, orow, t.ct * 128 + h * 64 + cp * 32, o, ov);
               emit(t.ct * 128 + h * 64 + cp * 32, o);
             }
             continue;
@@ -893,9 +891,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float cs1 = need_col ? cf[colt(c) + i] : 1.0f;
               o[i] = __uint_as_float(vv[i]) * s0 * cs1;
             }
-            if constexpr (kEpi) epi_apply(p, t.g, orow, col, o);
             emit(col, o);
           }
+        }
         }
         release_unit(buf);
         ++u;

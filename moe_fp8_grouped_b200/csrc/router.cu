@@ -18,6 +18,7 @@
 #include <cfloat>
 #include <cmath>
 
+#include "act.cuh"
 #include "internal.h"
 #include "router.h"
 
@@ -63,23 +64,28 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
-// log(sigmoid(x)) without overflow
-__device__ __forceinline__ float log_sigmoid(float x) { return fminf(x, 0.0f) - log1pf(expf(-fabsf(x))); }
+// exp(x): |x| 2^-23 relative from the product, 2 ulp from the unit
+__device__ __forceinline__ float fast_exp(float x) { return fast_exp2(x * kLog2e); }
 
-__device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
+// log(sigmoid(x)) without overflow
+__device__ __forceinline__ float log_sigmoid(float x) { return fminf(x, 0.0f) - log1pf(fast_exp(-fabsf(x))); }
+
+__device__ __forceinline__ float sigmoid(float x) { return fast_rcp(1.0f + fast_exp(-x)); }
 
 // One round of the choice: the lane's largest order with its lowest index,
 // then the warp's; the winner is removed.  Returns its index, -1 when nothing
-// is left, and its order in `best`.
+// is left, its order in `best` and its logit in `logit`.
 template <int kV, class T>
-__device__ __forceinline__ int take_largest(T (&ord)[kV], int lane, T &best) {
+__device__ __forceinline__ int take_largest(T (&ord)[kV], const float (&x)[kV], int lane, T &best, float &logit) {
   T m = ord[0];
   int v = 0;
+  float xv = x[0];
 #pragma unroll
   for (int i = 1; i < kV; ++i)
     if (ord[i] > m) {
       m = ord[i];
       v = i;
+      xv = x[i];
     }
   if constexpr (sizeof(T) == 4) {
     best = __reduce_max_sync(kFull, m);
@@ -93,6 +99,7 @@ __device__ __forceinline__ int take_largest(T (&ord)[kV], int lane, T &best) {
   }
   if (best == 0) return -1;
   const int e = __reduce_min_sync(kFull, m == best ? v * 32 + lane : 0x7fffffff);
+  logit = __shfl_sync(kFull, xv, e & 31);
 #pragma unroll
   for (int i = 0; i < kV; ++i)
     if (i * 32 + lane == e) ord[i] = 0;
@@ -109,11 +116,11 @@ __device__ __forceinline__ float chosen_weight(float xs, bool valid, float mx, f
     const float l = sig ? log_sigmoid(xs) : xs;
     const float m = warp_max(valid ? l : -INFINITY);
     const bool nan = __any_sync(kFull, valid && (isnan(l) || l == INFINITY));
-    const float e = valid ? expf(l - m) : 0.0f;
+    const float e = valid ? fast_exp(l - m) : 0.0f;
     const float s = warp_sum(e);
     return nan ? __int_as_float(0x7fffffff) : scale * (e / s);
   }
-  return sig ? scale * sigmoid(xs) : scale * (expf(xs - mx) / sum);
+  return sig ? scale * sigmoid(xs) : scale * (fast_exp(xs - mx) / sum);
 }
 
 template <int kV>
@@ -122,11 +129,12 @@ __global__ void __launch_bounds__(kRouterWarps * 32) router_topk_kernel(const Ro
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kRouterWarps + (threadIdx.x >> 5);
   if (t >= p.T) return;
   const int E = p.E, k = p.k;
-  float x[kV];
+  float x[kV], b[kV];
 #pragma unroll
   for (int i = 0; i < kV; ++i) {
     const int e = i * 32 + lane;
     x[i] = e < E ? load_logit(p.logits, t * E + e, p.bf16) : -INFINITY;
+    b[i] = p.bias && e < E ? p.bias[e] : 0.0f;
   }
   // softmax statistics of the row (not needed for sigmoid, nor when the
   // chosen weights are normalised and no bias is added to the scores)
@@ -139,31 +147,41 @@ __global__ void __launch_bounds__(kRouterWarps * 32) router_topk_kernel(const Ro
     mx = warp_max(m);
     float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kV; ++i) s += x[i] == -INFINITY ? 0.0f : expf(x[i] - mx);
+    for (int i = 0; i < kV; ++i) s += x[i] == -INFINITY ? 0.0f : fast_exp(x[i] - mx);
     sum = warp_sum(s);
   }
+  const float inv_sum = 1.0f / sum;
   uint32_t ord[kV];
 #pragma unroll
   for (int i = 0; i < kV; ++i) {
-    const int e = i * 32 + lane;
     float key = x[i];
-    if (p.bias && e < E && x[i] != -INFINITY) key = (sig ? sigmoid(x[i]) : expf(x[i] - mx) / sum) + p.bias[e];
+    if (p.bias && x[i] != -INFINITY) key = (sig ? sigmoid(x[i]) : fast_exp(x[i] - mx) * inv_sum) + b[i];
     ord[i] = order32(key);
   }
-  int mine = -1;   // lane j: expert of choice j
+  int mine = -1;  // lane j: expert of choice j, and its logit
+  float xs = 0.0f;
   bool near = false;
   uint32_t prev = 0;
+  // A key is within `off` + 2^-24 |key| of the true one: a sigmoid's error is
+  // s (1 - s) (|x| + 4) 2^-23 from the exponential, below 2e-7, and 1.5 ulp; a
+  // softmax score's, relative, (|x - m| + 8) 2^-23 and the sum's E / 32 + 5
+  // roundings, below 3e-6 of a score where that score is near the largest and
+  // absolutely below 3e-6 everywhere
+  const float off = sig ? 8e-7f : 6e-6f;  // of two keys
   for (int j = 0; j < k + (p.bias ? 1 : 0); ++j) {
     uint32_t o;
-    const int e = take_largest(ord, lane, o);
+    float xv;
+    const int e = take_largest(ord, x, lane, o, xv);
     if (e < 0) break;
     if (p.bias && j > 0) {
-      // both keys are within a few fp32 steps of the true ones
-      const float a = key_of_order32(prev), b = key_of_order32(o);
-      near |= !(a - b > 2e-6f + 1e-6f * fabsf(a));
+      const float a = key_of_order32(prev), c = key_of_order32(o);
+      near |= !(a - c > off + 2e-7f * (fabsf(a) + fabsf(c)));
     }
     prev = o;
-    if (lane == j && j < k) mine = e;
+    if (lane == j && j < k) {
+      mine = e;
+      xs = xv;
+    }
   }
   if (near) {
     double s64 = 1.0, m64 = mx;
@@ -181,19 +199,22 @@ __global__ void __launch_bounds__(kRouterWarps * 32) router_topk_kernel(const Ro
       const int e = i * 32 + lane;
       double key = x[i];
       if (e < E && x[i] != -INFINITY)
-        key = (sig ? 1.0 / (1.0 + exp(-key)) : exp(key - m64) / s64) + static_cast<double>(p.bias[e]);
+        key = (sig ? 1.0 / (1.0 + exp(-key)) : exp(key - m64) / s64) + static_cast<double>(b[i]);
       o64[i] = order64(key);
     }
     mine = -1;
     for (int j = 0; j < k; ++j) {
       unsigned long long o;
-      const int e = take_largest(o64, lane, o);
+      float xv;
+      const int e = take_largest(o64, x, lane, o, xv);
       if (e < 0) break;
-      if (lane == j) mine = e;
+      if (lane == j) {
+        mine = e;
+        xs = xv;
+      }
     }
   }
   const bool valid = lane < k && mine >= 0;
-  const float xs = valid ? load_logit(p.logits, t * E + mine, p.bf16) : 0.0f;
   const float w = chosen_weight(xs, valid, mx, sum, sig, p.normalize, p.scale);
   if (lane < k) {
     p.ids[t * k + lane] = mine;
@@ -221,14 +242,14 @@ __global__ void __launch_bounds__(kRouterWarps * 32) router_topk_bwd_kernel(cons
   if (p.normalize) {
     const float l = sig ? log_sigmoid(xs) : xs;
     const float m = warp_max(valid ? l : -INFINITY);
-    const float e = valid ? expf(l - m) : 0.0f;
+    const float e = valid ? fast_exp(l - m) : 0.0f;
     const float w = e / warp_sum(e);
     const float dot = warp_sum(valid ? w * dw : 0.0f);
     c = w * (dw - dot);
-    if (sig) c *= 1.0f / (1.0f + expf(xs));  // d log sigmoid = 1 - sigmoid
+    if (sig) c *= sigmoid(-xs);  // d log sigmoid = 1 - sigmoid
     for (int e2 = lane; e2 < E; e2 += 32) row[e2] = 0.0f;
   } else if (sig) {
-    c = dw * sigmoid(xs) * (1.0f / (1.0f + expf(xs)));
+    c = dw * sigmoid(xs) * sigmoid(-xs);
     for (int e2 = lane; e2 < E; e2 += 32) row[e2] = 0.0f;
   } else {
     float m = -INFINITY;
@@ -240,12 +261,12 @@ __global__ void __launch_bounds__(kRouterWarps * 32) router_topk_bwd_kernel(cons
     m = warp_max(m);
     float s = 0.0f;
     for (int e2 = lane; e2 < E; e2 += 32) {
-      const float e = row[e2] == -INFINITY ? 0.0f : expf(row[e2] - m);
+      const float e = row[e2] == -INFINITY ? 0.0f : fast_exp(row[e2] - m);
       row[e2] = e;
       s += e;
     }
     s = warp_sum(s);
-    const float pr = valid ? expf(xs - m) / s : 0.0f;
+    const float pr = valid ? fast_exp(xs - m) / s : 0.0f;
     c = pr * dw;
     const float dot = warp_sum(valid ? c : 0.0f);
     const float f = s > 0.0f ? dot / s : 0.0f;

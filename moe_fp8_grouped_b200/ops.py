@@ -6,7 +6,9 @@ and a reusable workspace) and the stream.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 
 import torch
 
@@ -338,10 +340,41 @@ def _name(table: dict, name, what: str) -> int:
     return table[name]
 
 
-def _same_device(first: torch.Tensor, **others):
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} is on {t.device}, expected {first.device}")
+def _same_device(first: torch.Tensor, *others):
+    dev = first.device
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {t.device} and {dev}: all must be on one device")
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_here = contextlib.nullcontext()
+
+
+def _on(t: torch.Tensor):
+    """Makes t's device current for the call (nothing to do when it is)."""
+    return _here if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+
+
+def _current(t: torch.Tensor) -> int:
+    """The raw handle of torch's current stream on t's device, without the
+    Python stream object (a microsecond of the smallest calls)."""
+    return _raw_stream(t.device.index) if _raw_stream else _stream(t)
+
+
+@functools.lru_cache(maxsize=4096)
+def _fwd_bytes(M: int, K: int, N: int, G: int) -> int:
+    return gmm_workspace_bytes(B.OP_FWD, M, K, N, G)
+
+
+@functools.lru_cache(maxsize=4096)
+def _act_bwd_bytes(M: int, N: int, G: int) -> int:
+    return int(B.lib().gmm_act_bwd_workspace_bytes(M, N, G))
+
+
+@functools.lru_cache(maxsize=4096)
+def _few_bytes(T: int, k: int, G: int, K: int, F: int, N: int, dtype: int) -> int:
+    return int(B.lib().gmm_moe_few_workspace_bytes(T, k, G, K, F, N, dtype))
 
 
 def _shape(t: torch.Tensor | None, name: str, shape):
@@ -381,8 +414,7 @@ def gmm_fwd_act(lhs: torch.Tensor, rhs: torch.Tensor, rhs_scales: torch.Tensor |
     _shape(out, "out", out_shape)
     _shape(preact, "preact", (M, N))
     _shape(group_sizes, "group_sizes", (G,))
-    _same_device(lhs, rhs=rhs, rhs_scales=rhs_scales, group_sizes=group_sizes, bias=bias, residual=residual, out=out,
-                 ws=ws, preact=preact, static_scale=static_scale, lhs_scales=lhs_scales)
+    _same_device(lhs, rhs, rhs_scales, group_sizes, bias, residual, out, ws, preact, static_scale, lhs_scales)
     if lhs.dtype in (torch.uint8, torch.float8_e4m3fn):
         sc = static_scale if r == B.Q_STATIC else lhs_scales
         a = _operand(_dev(lhs, "lhs"), B.DT_E4M3, _dev(sc, "lhs scale", torch.float32), r)
@@ -396,12 +428,12 @@ def gmm_fwd_act(lhs: torch.Tensor, rhs: torch.Tensor, rhs_scales: torch.Tensor |
                      _dev(residual, "residual", (torch.bfloat16, torch.float32)),
                      _TORCH_DT[residual.dtype] if residual is not None else B.DT_BF16,
                      _dev(preact, "preact", torch.bfloat16))
-    with torch.cuda.device(lhs.device):
-        ws = _scratch(ws, gmm_workspace_bytes(B.OP_FWD, M, K, N, G), lhs.device)
+    with _on(lhs):
+        ws = _scratch(ws, _fwd_bytes(M, K, N, G), lhs.device)
         st = B.lib().gmm_fwd_act(a, _rhs_operand(rhs, rhs_scales), int(transpose_rhs),
                                  _dev(group_sizes, "group_sizes", torch.int32), G, M, K, N, ctypes.byref(epi),
                                  _dev(out, "out", (torch.bfloat16, torch.float32)), _TORCH_DT[out.dtype],
-                                 _dev(ws, "ws"), ws.numel(), _stream(lhs))
+                                 _dev(ws, "ws"), ws.numel(), _current(lhs))
     _check(st, "gmm_fwd_act")
     return out if preact is None else (out, preact)
 
@@ -418,17 +450,17 @@ def gmm_act_bwd(dout: torch.Tensor, preact: torch.Tensor, group_sizes: torch.Ten
     _shape(dout, "dout", (M, N // 2 if act == "swiglu" else N))
     _shape(dz, "dz", (M, N))
     _shape(dbias, "dbias", (G, N))
-    _same_device(dout, preact=preact, group_sizes=group_sizes, dz=dz, dbias=dbias, ws=ws)
+    _same_device(dout, preact, group_sizes, dz, dbias, ws)
     if dz is None:
         dz = torch.empty((M, N), dtype=torch.bfloat16, device=dout.device)
     if dbias is None and with_dbias:
         dbias = torch.empty((G, N), dtype=torch.float32, device=dout.device)
-    with torch.cuda.device(dout.device):
-        ws = _scratch(ws, int(B.lib().gmm_act_bwd_workspace_bytes(M, N, G)), dout.device)
+    with _on(dout):
+        ws = _scratch(ws, _act_bwd_bytes(M, N, G), dout.device)
         st = B.lib().gmm_act_bwd(_dev(dout, "dout", torch.bfloat16), _dev(preact, "preact", torch.bfloat16), a_code,
                                  _dev(group_sizes, "group_sizes", torch.int32), G, M, N,
                                  _dev(dz, "dz", torch.bfloat16), _dev(dbias, "dbias", torch.float32), _dev(ws, "ws"),
-                                 ws.numel(), _stream(dout))
+                                 ws.numel(), _current(dout))
     _check(st, "gmm_act_bwd")
     return dz, dbias
 
@@ -455,22 +487,21 @@ def gmm_moe_few(x: torch.Tensor, expert_ids: torch.Tensor, weights: torch.Tensor
     _shape(w1_scales, "w1_scales", (G, F2))
     _shape(w2_scales, "w2_scales", (G, N))
     _shape(out, "out", (T, N))
-    _same_device(x, expert_ids=expert_ids, weights=weights, w1=w1, w1_scales=w1_scales, w2=w2, w2_scales=w2_scales,
-                 out=out, ws=ws)
+    _same_device(x, expert_ids, weights, w1, w1_scales, w2, w2_scales, out, ws)
     if w1.dtype not in _TORCH_DT or w2.dtype not in _TORCH_DT:
         raise ValueError(f"w1 / w2 have dtype {w1.dtype} / {w2.dtype}, expected E4M3 codes or bf16")
     dt = _TORCH_DT[w1.dtype]
     if out is None:
         out = torch.empty((T, N), dtype=out_dtype, device=x.device)
-    with torch.cuda.device(x.device):
-        ws = _scratch(ws, int(B.lib().gmm_moe_few_workspace_bytes(T, k, G, K, F, N, dt)), x.device)
+    with _on(x):
+        ws = _scratch(ws, _few_bytes(T, k, G, K, F, N, dt), x.device)
         st = B.lib().gmm_moe_few(
             _dev(x, "x", torch.bfloat16), _dev(expert_ids, "expert_ids", torch.int32),
             _dev(weights, "weights", torch.float32), T, k,
             _operand(_dev(w1, "w1"), dt, _dev(w1_scales, "w1_scales", torch.float32), B.Q_NONE),
             _operand(_dev(w2, "w2"), _TORCH_DT[w2.dtype], _dev(w2_scales, "w2_scales", torch.float32), B.Q_NONE),
             int(transpose_rhs), G, K, F, N, _dev(out, "out", (torch.bfloat16, torch.float32)), _TORCH_DT[out.dtype],
-            _dev(ws, "ws"), ws.numel(), _stream(x))
+            _dev(ws, "ws"), ws.numel(), _current(x))
     _check(st, "gmm_moe_few")
     return out
 
@@ -484,14 +515,14 @@ def gmm_router_topk(logits: torch.Tensor, k: int, score: str = "softmax", select
     never chosen (id -1, weight 0 where fewer than k are left)."""
     T, E = logits.shape
     _shape(select_bias, "select_bias", (E,))
-    _same_device(logits, select_bias=select_bias)
+    _same_device(logits, select_bias)
     ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
     weights = torch.empty((T, k), dtype=torch.float32, device=logits.device)
-    with torch.cuda.device(logits.device):
+    with _on(logits):
         st = B.lib().gmm_router_topk(_dev(logits, "logits", (torch.float32, torch.bfloat16)), _TORCH_DT[logits.dtype],
                                      T, E, k, _name(SCORES, score, "score"),
                                      _dev(select_bias, "select_bias", torch.float32), int(normalize), float(scale),
-                                     ids.data_ptr(), weights.data_ptr(), _stream(logits))
+                                     ids.data_ptr(), weights.data_ptr(), _current(logits))
     _check(st, "gmm_router_topk")
     return ids, weights
 
@@ -504,14 +535,14 @@ def gmm_router_topk_bwd(dweights: torch.Tensor, logits: torch.Tensor, expert_ids
     k = expert_ids.shape[1]
     _shape(expert_ids, "expert_ids", (T, k))
     _shape(dweights, "dweights", (T, k))
-    _same_device(logits, dweights=dweights, expert_ids=expert_ids)
+    _same_device(logits, dweights, expert_ids)
     dlogits = torch.empty_like(logits)
-    with torch.cuda.device(logits.device):
+    with _on(logits):
         st = B.lib().gmm_router_topk_bwd(_dev(dweights, "dweights", torch.float32),
                                          _dev(logits, "logits", (torch.float32, torch.bfloat16)),
                                          _TORCH_DT[logits.dtype], _dev(expert_ids, "expert_ids", torch.int32), T, E, k,
                                          _name(SCORES, score, "score"), int(normalize), float(scale),
-                                         dlogits.data_ptr(), _stream(logits))
+                                         dlogits.data_ptr(), _current(logits))
     _check(st, "gmm_router_topk_bwd")
     return dlogits
 
@@ -522,12 +553,12 @@ def gmm_combine_dweight(dy: torch.Tensor, rows: torch.Tensor, slot: torch.Tensor
     rows).  dy [T, N] and rows [R, N] bf16, slot int32 [T, k]."""
     T, k = slot.shape
     _shape(dy, "dy", (T, rows.shape[1]))
-    _same_device(dy, rows=rows, slot=slot)
+    _same_device(dy, rows, slot)
     dw = torch.empty((T, k), dtype=torch.float32, device=dy.device)
-    with torch.cuda.device(dy.device):
+    with _on(dy):
         st = B.lib().gmm_combine_dweight(_dev(dy, "dy", torch.bfloat16), _dev(rows, "rows", torch.bfloat16),
                                          rows.shape[0], _dev(slot, "slot", torch.int32), T, k, rows.shape[1],
-                                         dw.data_ptr(), _stream(dy))
+                                         dw.data_ptr(), _current(dy))
     _check(st, "gmm_combine_dweight")
     return dw
 

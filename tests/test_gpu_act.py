@@ -164,14 +164,17 @@ def test_fwd_every_tile(tiles, rule, act, trans):
 
 
 def test_plain_epilogue_equals_gmm_fwd():
-    """No bias, no activation, no residual: the bits of gmm_fwd / gmm_fwd_swiglu."""
+    """No bias, no activation, no residual: the bits of gmm_fwd; with SwiGLU
+    gmm_fwd_swiglu up to the evaluation of silu (1e-5 of the value each, so
+    that a bf16 result differs by one step at most: 2^-7 of itself)."""
     lhs, w, _, gs, s = _case([200, 0, 56], 300, 384, 512, 3)
     codes, sc = gm.gmm_quantize_rhs(w)
     for rule in ("static", "dynamic"):
         kw = dict(rule=rule, static_scale=s if rule == "static" else None)
         assert torch.equal(gm.gmm_fwd_act(lhs, codes, sc, gs, **kw), gm.gmm_fwd(lhs, codes, sc, gs, **kw))
-        assert torch.equal(gm.gmm_fwd_act(lhs, codes, sc, gs, act="swiglu", **kw),
-                           gm.gmm_fwd_swiglu(lhs, codes, sc, gs, **kw))
+        a = gm.gmm_fwd_act(lhs, codes, sc, gs, act="swiglu", **kw).double()
+        b = gm.gmm_fwd_swiglu(lhs, codes, sc, gs, **kw).double()
+        assert bool(((a - b).abs() <= 2.0 ** -7 * b.abs()).all())
 
 
 def test_block_scaled_weights_and_quantized_lhs():
