@@ -416,7 +416,8 @@ static gmm_status fwd_impl(gmm_operand lhs, gmm_operand rhs, int transpose_rhs, 
   }
   const bool bmn = transpose_rhs == 0;  // [G, K, N]: N contiguous = MN-major B
   const uint32_t bke = 128 / elem;
-  const bool pairs = use_pairs(false, M, N, G, elem, dyn || blk);
+  // (a promoted product with a fused epilogue has no pair tiles)
+  const bool pairs = use_pairs(false, M, N, G, elem, dyn || blk) && !(epi && elem == 1 && (dyn || blk));
   CUtensorMap tmA, tmB;
   if (!make_map(&tmA, A, elem, K, M, K * elem, bke, 128)) return GMM_ERR_CUDA;
   // SwiGLU tiles take the gate rows and the up rows of a K-major rhs as two

@@ -3,7 +3,7 @@
 // activation and the residual.
 //
 // The E4M3 passes hold a thread's 128 accumulators in registers and finish them
-// 32 columns at a time (16 at a time, with narrower stores, ran 5 % slower; a
+// 32 columns at a time, in one instantiation per activation (16 columns at a time, with narrower stores, ran 5 % slower; a
 // rolled loop over shifted accumulators 40 %: it spills them); the bf16 family
 // reads its chunks from TMEM in one rolled loop.  The activations' instructions
 // are what an epilogue is made of: with the exact library forms of act.cuh's
@@ -160,7 +160,7 @@ __device__ __forceinline__ void epi_act(float2 (&o)[kPairs]) {
 
 // One chunk: o holds the products of row `row`, columns col .. (for SwiGLU the
 // gate columns, u the matching up columns); writes the outputs.
-template <int kPairs>
+template <int kEpi, int kPairs>
 __device__ __forceinline__ void epi_finish(const GemmParams &p, int g, int64_t row, bool sw, int col,
                                            float2 (&o)[kPairs], float2 (&u)[kPairs], bool out_v8) {
   const int64_t off = row * p.ld_out + col;
@@ -174,6 +174,8 @@ __device__ __forceinline__ void epi_finish(const GemmParams &p, int g, int64_t r
     epi_act<GMM_ACT_SILU>(o);
 #pragma unroll
     for (int i = 0; i < kPairs; ++i) o[i] = __fmul2_rn(o[i], u[i]);
+  } else if constexpr (kEpi >= 0) {
+    epi_act<kEpi>(o);
   } else {
     switch (p.act) {
       case GMM_ACT_RELU: epi_act<GMM_ACT_RELU>(o); break;
@@ -193,11 +195,12 @@ __device__ __forceinline__ void epi_finish(const GemmParams &p, int g, int64_t r
   }
 }
 
-// products of 32 tile columns: acc * before * cf[column] * after
+// products of 32 tile columns: acc (* before) * cf[column] (* after)
+template <bool kBefore, bool kAfter>
 __device__ __forceinline__ void epi_products(const float2 *acc, const float *cf, bool scaled, float before,
                                              float after, float2 (&o)[16]) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) o[i] = __fmul2_rn(acc[i], splat(before));
+  for (int i = 0; i < 16; ++i) o[i] = kBefore ? __fmul2_rn(acc[i], splat(before)) : acc[i];
   if (scaled) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -206,33 +209,35 @@ __device__ __forceinline__ void epi_products(const float2 *acc, const float *cf,
       o[2 * i + 1] = __fmul2_rn(o[2 * i + 1], make_float2(s.z, s.w));
     }
   }
+  if constexpr (kAfter) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) o[i] = __fmul2_rn(o[i], splat(after));
+    for (int i = 0; i < 16; ++i) o[i] = __fmul2_rn(o[i], splat(after));
+  }
 }
 
 // A thread's kCh * 32 tile columns (column half h of column tile ct; for
 // SwiGLU 64 gate columns, then the matching 64 up columns); cf: the tile's
 // column scales in shared memory (scaled: there are any).
-template <int kCh>
-__device__ __forceinline__ void epi_tile(const GemmParams &p, int g, int64_t row, int ct, int h, bool sw,
+template <int kCh, int kEpi, bool kBefore, bool kAfter>
+__device__ __forceinline__ void epi_tile(const GemmParams &p, int g, int64_t row, int ct, int h,
                                          const float2 (&acc)[kCh * 16], const float *cf, bool scaled, float before,
                                          float after, bool out_v8) {
   float2 o[16], u[16];
-  if (kCh == 4 && sw) {
+  if constexpr (kEpi == GMM_ACT_SWIGLU) {
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int in_tile = h * 64 + c * 32;
-      epi_products(acc + c * 16, cf + in_tile, scaled, before, after, o);
-      epi_products(acc + (32 + c * 16) % (kCh * 16), cf + 128 + in_tile, scaled, before, after, u);
-      epi_finish(p, g, row, true, ct * 128 + in_tile, o, u, out_v8);
+      epi_products<kBefore, kAfter>(acc + c * 16, cf + in_tile, scaled, before, after, o);
+      epi_products<kBefore, kAfter>(acc + (32 + c * 16) % (kCh * 16), cf + 128 + in_tile, scaled, before, after, u);
+      epi_finish<kEpi>(p, g, row, true, ct * 128 + in_tile, o, u, out_v8);
     }
   } else {
 #pragma unroll
     for (int c = 0; c < kCh; ++c) {
       const int in_tile = h * kCh * 32 + c * 32, col = ct * kCh * 64 + in_tile;
       if (col >= p.ncols) continue;
-      epi_products(acc + c * 16, cf + in_tile, scaled, before, after, o);
-      epi_finish(p, g, row, false, col, o, u, out_v8);
+      epi_products<kBefore, kAfter>(acc + c * 16, cf + in_tile, scaled, before, after, o);
+      epi_finish<kEpi>(p, g, row, false, col, o, u, out_v8);
     }
   }
 }
@@ -248,7 +253,7 @@ __device__ __forceinline__ void epi_chunk(const GemmParams &p, int g, int64_t ro
     o[i] = make_float2(__uint_as_float(va[2 * i]), __uint_as_float(va[2 * i + 1]));
     if (sw) u[i] = make_float2(__uint_as_float(vb[2 * i]), __uint_as_float(vb[2 * i + 1]));
   }
-  epi_finish(p, g, row, sw, col, o, u, out_v8);
+  epi_finish<kAnyEpi>(p, g, row, sw, col, o, u, out_v8);
 }
 
 }  // namespace gmm

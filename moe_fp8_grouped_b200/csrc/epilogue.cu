@@ -20,7 +20,7 @@ namespace {
 constexpr int kActThreads = 256;
 constexpr int kActCols = 256;  // columns of a CTA: 32 threads of 8
 constexpr int kActRowThreads = kActThreads / 32;
-constexpr int kActUnroll = 4;
+constexpr int kActUnroll = 1;
 
 __device__ __forceinline__ float2 bf16x2_f32(uint32_t v) {
   return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
@@ -35,7 +35,7 @@ __device__ __forceinline__ uint4 pack8(const float2 (&v)[4]) {
 }
 
 template <int kAct>
-__global__ void __launch_bounds__(kActThreads) act_bwd_kernel(const ActBwdParams p) {
+__global__ void __launch_bounds__(kActThreads, 4) act_bwd_kernel(const ActBwdParams p) {
   constexpr bool kGated = kAct == GMM_ACT_SWIGLU;
   constexpr int kParts = kGated ? 2 : 1;
   __shared__ float s_sum[kActRowThreads][kParts][kActCols];

@@ -174,7 +174,7 @@ __device__ __forceinline__ void store_col32(void *out, int64_t off_elems, int64_
 // kTN: tile columns, 256, or 128 for CTA pairs in the promoted passes with a
 // K-major B (four 128-column TMEM buffers instead of two of 256: the MMA can
 // run three units ahead of the epilogue).
-template <int kElem, bool kBMN, bool kPromote, int kMode, int kTN, bool kEpi>
+template <int kElem, bool kBMN, bool kPromote, int kMode, int kTN, int kEpi>
 __global__ void __launch_bounds__(kThreads, 1)
     gmm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmOut, const GemmParams p) {
@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q = warp & 3, h = (warp - kEpiWarp0) >> 2;
     const int row = q * 32 + lane;
     const uint32_t tl = tbase + (static_cast<uint32_t>(q * 32) << 16);  // the warp's TMEM lanes
-    const bool sw = !kTg && p.swiglu_f > 0;
+    const bool sw = kEpi >= 0 ? kEpi == GMM_ACT_SWIGLU : !kTg && p.swiglu_f > 0;
     // tile column of the thread's 32-column chunk c (0 .. 3): the column half h
     // of the tile, or for SwiGLU gate columns 64 h .. (c = 0, 1) and the
     // matching up columns 128 + 64 h .. (c = 2, 3)
@@ -614,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         orow = static_cast<int64_t>(t.rt) * kBM + row;  // n
         row_ok = true;
       }
-      if constexpr (kEpi) {
+      if constexpr (kEpi != kNoEpi) {
         if (row_ok) epi_prefetch(p, orow, sw ? t.ct * 128 + h * 64 : col0, sw ? 64 : kTN / 2);
       }
       // writes 32 tile columns starting at tile column col (a multiple of 32)
@@ -717,10 +717,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (b + 1 < t.nblocks) release_slot(slot);  // the last slot is read again below
         }
         if (!ok) break;
-        if constexpr (kEpi) {
+        if constexpr (kEpi != kNoEpi) {
           if (row_ok)
-            epi_tile<kCh>(p, t.g, orow, t.ct, h, sw, acc, s_scol + slot * kBN, p.col_scale != nullptr, 1.0f,
-                        (kBlkScales && p.static_scale) ? s_eff : 1.0f, out_v8);
+            epi_tile<kCh, kEpi, false, kBlkScales>(p, t.g, orow, t.ct, h, acc, s_scol + slot * kBN,
+                                                 p.col_scale != nullptr, 1.0f, p.static_scale ? s_eff : 1.0f,
+                                                 out_v8);
         } else if (row_ok) {
           // per-channel rhs column scale (in every unit's slot); static lhs: s
           const float fin = ((kTg || kBlkScales) && p.static_scale) ? s_eff : 1.0f;
@@ -798,10 +799,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (two) release_unit(1);
         ++n0;
         if (two) ++n1;
-        if constexpr (kEpi) {
+        if constexpr (kEpi != kNoEpi) {
           if (row_ok)
-            epi_tile<4>(p, t.g, orow, t.ct, h, sw, acc, s_scol + slot * kBN, need_col,
-                        p.static_scale ? s_eff : 1.0f, 1.0f, out_v8);
+            epi_tile<4, kEpi, true, false>(p, t.g, orow, t.ct, h, acc, s_scol + slot * kBN, need_col,
+                                           p.static_scale ? s_eff : 1.0f, 1.0f, out_v8);
         } else if (row_ok) {
           const float s0 = p.static_scale ? s_eff : 1.0f;
           const float *cf = s_scol + slot * kBN;
@@ -846,7 +847,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
-        if constexpr (kEpi && kElem == 2) {
+        if constexpr (kEpi != kNoEpi && kElem == 2) {
           // chunk by chunk from TMEM, in one copy of the epilogue's code
 #pragma unroll 1
           for (int c = 0; c < (sw ? 2 : 4); ++c) {
@@ -854,46 +855,48 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld32(tl + buf * kTN + colt(c), va);
             if (sw) tmem_ld32(tl + buf * kTN + colt(c + 2), vb);
             tmem_wait_ld();
-            if (row_ok) epi_chunk(p, t.g, orow, sw, sw ? t.ct * 128 + h * 64 + c * 32 : t.ct * kTN + colt(c), va, vb, out_v8);
+            if (row_ok)
+              epi_chunk(p, t.g, orow, sw, sw ? t.ct * 128 + h * 64 + c * 32 : t.ct * kTN + colt(c), va, vb,
+                        out_v8);
           }
         } else {
-        const float s0 = p.static_scale ? s_eff : 1.0f;
-        const float *cf = s_scol + slot * kBN;
+          const float s0 = p.static_scale ? s_eff : 1.0f;
+          const float *cf = s_scol + slot * kBN;
 #pragma unroll
-        for (int cp = 0; cp < 2; ++cp) {
-          const int ca = sw ? cp : 2 * cp, cb = sw ? cp + 2 : 2 * cp + 1;
-          uint32_t va[32], vb[32];
-          tmem_ld32(tl + buf * kTN + colt(ca), va);
-          tmem_ld32(tl + buf * kTN + colt(cb), vb);
-          tmem_wait_ld();
-          if (sw) {
-            if (row_ok) {
-              const float *fg = cf + colt(ca), *fu = cf + colt(cb);
+          for (int cp = 0; cp < 2; ++cp) {
+            const int ca = sw ? cp : 2 * cp, cb = sw ? cp + 2 : 2 * cp + 1;
+            uint32_t va[32], vb[32];
+            tmem_ld32(tl + buf * kTN + colt(ca), va);
+            tmem_ld32(tl + buf * kTN + colt(cb), vb);
+            tmem_wait_ld();
+            if (sw) {
+              if (row_ok) {
+                const float *fg = cf + colt(ca), *fu = cf + colt(cb);
+                float o[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                  const float gs = need_col ? fg[i] : 1.0f, us = need_col ? fu[i] : 1.0f;
+                  o[i] = silu(__uint_as_float(va[i]) * s0 * gs) * (__uint_as_float(vb[i]) * s0 * us);
+                }
+                emit(t.ct * 128 + h * 64 + cp * 32, o);
+              }
+              continue;
+            }
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const uint32_t *vv = half ? vb : va;
+              const int c = half ? cb : ca;
+              const int col = t.ct * kTN + colt(c);
+              if (!row_ok || col >= p.ncols) continue;
               float o[32];
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
-                const float gs = need_col ? fg[i] : 1.0f, us = need_col ? fu[i] : 1.0f;
-                o[i] = silu(__uint_as_float(va[i]) * s0 * gs) * (__uint_as_float(vb[i]) * s0 * us);
+                const float cs1 = need_col ? cf[colt(c) + i] : 1.0f;
+                o[i] = __uint_as_float(vv[i]) * s0 * cs1;
               }
-              emit(t.ct * 128 + h * 64 + cp * 32, o);
+              emit(col, o);
             }
-            continue;
           }
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const uint32_t *vv = half ? vb : va;
-            const int c = half ? cb : ca;
-            const int col = t.ct * kTN + colt(c);
-            if (!row_ok || col >= p.ncols) continue;
-            float o[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float cs1 = need_col ? cf[colt(c) + i] : 1.0f;
-              o[i] = __uint_as_float(vv[i]) * s0 * cs1;
-            }
-            emit(col, o);
-          }
-        }
         }
         release_unit(buf);
         ++u;
@@ -917,7 +920,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + (r * p.ld_out) * esz + c * 16) =
             make_uint4(0, 0, 0, 0);
       }
-      if constexpr (kEpi) {  // the kept pre-activations too
+      if constexpr (kEpi != kNoEpi) {  // the kept pre-activations too
         const int64_t zc = p.ncols / 8, zn = p.preact ? (static_cast<int64_t>(p.M) - tail0) * zc : 0;
         for (int64_t i = static_cast<int64_t>(blockIdx.x) * kEpiThreads + et; i < zn;
              i += static_cast<int64_t>(gridDim.x) * kEpiThreads)
@@ -938,7 +941,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int kElem, bool kBMN, bool kPromote, int kMode, int kTN = 256, bool kEpi = false>
+template <int kElem, bool kBMN, bool kPromote, int kMode, int kTN = 256, int kEpi = kNoEpi>
 static cudaError_t launch_inst(const CUtensorMap &tmA, const CUtensorMap &tmB, const CUtensorMap &tmOut,
                                const GemmParams &p, int items, cudaStream_t st) {
   auto kern = gmm_pair_kernel<kElem, kBMN, kPromote, kMode, kTN, kEpi>;
@@ -978,36 +981,50 @@ static cudaError_t launch_inst(const CUtensorMap &tmA, const CUtensorMap &tmB, c
   return cudaLaunchKernelEx(&cfg, kern, tmA, tmB, tmOut, p);
 }
 
-// the row passes (forward, dlhs); kEpi: with bias, activation and residual
-template <bool kEpi>
+// the static E4M3 row passes with a fused epilogue (the promoted ones, slower
+// on pairs without one, take one-CTA tiles)
+template <int kEpi>
+static cudaError_t launch_static_act(const GemmConfig &cfg, const CUtensorMap &tmA, const CUtensorMap &tmB,
+                                     const CUtensorMap &tmOut, const GemmParams &p, int items, cudaStream_t st) {
+  return cfg.b_mn_major ? launch_inst<1, true, false, MODE_ROWS, 256, kEpi>(tmA, tmB, tmOut, p, items, st)
+                        : launch_inst<1, false, false, MODE_ROWS, 256, kEpi>(tmA, tmB, tmOut, p, items, st);
+}
+
+#ifndef GMM_EPI_ACT  // (gemm_act_*.cu include this file for launch_static_act)
+
+// the row passes (forward, dlhs)
 static cudaError_t launch_rows(const GemmConfig &cfg, const CUtensorMap &tmA, const CUtensorMap &tmB,
                                const CUtensorMap &tmOut, const GemmParams &p, int items, cudaStream_t st) {
   if (cfg.tile_n == 128) {  // four 128-column TMEM buffers: promoted E4M3, K-major B
     if (cfg.elem_bytes != 1 || !cfg.promote || cfg.b_mn_major || p.swiglu_f) return cudaErrorInvalidValue;
-    if (cfg.mode == MODE_ROWS) return launch_inst<1, false, true, MODE_ROWS, 128, kEpi>(tmA, tmB, tmOut, p, items, st);
+    if (cfg.mode == MODE_ROWS) return launch_inst<1, false, true, MODE_ROWS, 128>(tmA, tmB, tmOut, p, items, st);
     if (cfg.mode == MODE_ROWS_BLK)
-      return launch_inst<1, false, true, MODE_ROWS_BLK, 128, kEpi>(tmA, tmB, tmOut, p, items, st);
+      return launch_inst<1, false, true, MODE_ROWS_BLK, 128>(tmA, tmB, tmOut, p, items, st);
     return cudaErrorInvalidValue;
   }
   if (cfg.tile_n != 256) return cudaErrorInvalidValue;
   if (cfg.mode == MODE_ROWS_BLK) {  // block-wise rhs scales: promoted fp8 only
     if (cfg.elem_bytes != 1 || !cfg.promote) return cudaErrorInvalidValue;
-    return cfg.b_mn_major ? launch_inst<1, true, true, MODE_ROWS_BLK, 256, kEpi>(tmA, tmB, tmOut, p, items, st)
-                          : launch_inst<1, false, true, MODE_ROWS_BLK, 256, kEpi>(tmA, tmB, tmOut, p, items, st);
+    return cfg.b_mn_major ? launch_inst<1, true, true, MODE_ROWS_BLK, 256>(tmA, tmB, tmOut, p, items, st)
+                          : launch_inst<1, false, true, MODE_ROWS_BLK, 256>(tmA, tmB, tmOut, p, items, st);
   }
   if (cfg.elem_bytes == 1) {
     if (cfg.b_mn_major)
-      return cfg.promote ? launch_inst<1, true, true, MODE_ROWS, 256, kEpi>(tmA, tmB, tmOut, p, items, st)
-                         : launch_inst<1, true, false, MODE_ROWS, 256, kEpi>(tmA, tmB, tmOut, p, items, st);
-    return cfg.promote ? launch_inst<1, false, true, MODE_ROWS, 256, kEpi>(tmA, tmB, tmOut, p, items, st)
-                       : launch_inst<1, false, false, MODE_ROWS, 256, kEpi>(tmA, tmB, tmOut, p, items, st);
+      return cfg.promote ? launch_inst<1, true, true, MODE_ROWS, 256>(tmA, tmB, tmOut, p, items, st)
+                         : launch_inst<1, true, false, MODE_ROWS, 256>(tmA, tmB, tmOut, p, items, st);
+    return cfg.promote ? launch_inst<1, false, true, MODE_ROWS, 256>(tmA, tmB, tmOut, p, items, st)
+                       : launch_inst<1, false, false, MODE_ROWS, 256>(tmA, tmB, tmOut, p, items, st);
   }
   if (cfg.promote) return cudaErrorInvalidValue;
-  return cfg.b_mn_major ? launch_inst<2, true, false, MODE_ROWS, 256, kEpi>(tmA, tmB, tmOut, p, items, st)
-                        : launch_inst<2, false, false, MODE_ROWS, 256, kEpi>(tmA, tmB, tmOut, p, items, st);
+  return cfg.b_mn_major ? launch_inst<2, true, false, MODE_ROWS, 256>(tmA, tmB, tmOut, p, items, st)
+                        : launch_inst<2, false, false, MODE_ROWS, 256>(tmA, tmB, tmOut, p, items, st);
 }
 
+#endif  // GMM_EPI_ACT
+
 }  // namespace pair
+
+#ifndef GMM_EPI_ACT
 
 cudaError_t launch_gemm_pair(const GemmConfig &cfg, const CUtensorMap &tmA, const CUtensorMap &tmB,
                              const CUtensorMap &tmOut, const GemmParams &p, int items, cudaStream_t st) {
@@ -1024,8 +1041,14 @@ cudaError_t launch_gemm_pair(const GemmConfig &cfg, const CUtensorMap &tmA, cons
       return launch_inst<2, false, false, MODE_TGMM>(tmA, tmB, tmOut, p, items, st);
     return cudaErrorInvalidValue;
   }
-  return cfg.epilogue ? launch_rows<true>(cfg, tmA, tmB, tmOut, p, items, st)
-                      : launch_rows<false>(cfg, tmA, tmB, tmOut, p, items, st);
+  if (cfg.epilogue) {  // bf16 family: every activation in one instantiation
+    if (cfg.elem_bytes != 2 || cfg.promote || cfg.mode != MODE_ROWS) return cudaErrorInvalidValue;
+    return cfg.b_mn_major ? launch_inst<2, true, false, MODE_ROWS, 256, kAnyEpi>(tmA, tmB, tmOut, p, items, st)
+                          : launch_inst<2, false, false, MODE_ROWS, 256, kAnyEpi>(tmA, tmB, tmOut, p, items, st);
+  }
+  return launch_rows(cfg, tmA, tmB, tmOut, p, items, st);
 }
+
+#endif  // GMM_EPI_ACT
 
 }  // namespace gmm

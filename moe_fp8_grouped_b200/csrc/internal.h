@@ -148,4 +148,39 @@ cudaError_t launch_gemm(const GemmConfig &cfg, const CUtensorMap &tmA, const CUt
 cudaError_t launch_gemm_pair(const GemmConfig &cfg, const CUtensorMap &tmA, const CUtensorMap &tmB,
                              const CUtensorMap &tmOut, const GemmParams &p, int items, cudaStream_t st);
 
+// Epilogue of a GEMM instantiation: kNoEpi the plain product, kAnyEpi a fused
+// epilogue whose activation is read at run time (bf16 family), else the
+// gmm_act it is compiled for (gemm_act_*.cu).
+constexpr int kNoEpi = -2, kAnyEpi = -1;
+
+// The E4M3 row passes with a fused epilogue, by activation.  cfg.cta_pairs:
+// static rule only.
+template <int kAct>
+cudaError_t launch_gemm_act_of(const GemmConfig &cfg, const CUtensorMap &tmA, const CUtensorMap &tmB,
+                               const CUtensorMap &tmOut, const GemmParams &p, int grid, cudaStream_t st);
+#define GMM_DECLARE_ACT(A)                                                                                  \
+  template <>                                                                                               \
+  cudaError_t launch_gemm_act_of<A>(const GemmConfig &cfg, const CUtensorMap &tmA, const CUtensorMap &tmB, \
+                                    const CUtensorMap &tmOut, const GemmParams &p, int grid, cudaStream_t st);
+GMM_DECLARE_ACT(0)
+GMM_DECLARE_ACT(1)
+GMM_DECLARE_ACT(2)
+GMM_DECLARE_ACT(3)
+GMM_DECLARE_ACT(4)
+GMM_DECLARE_ACT(5)
+#undef GMM_DECLARE_ACT
+
+inline cudaError_t launch_gemm_act(const GemmConfig &cfg, const CUtensorMap &tmA, const CUtensorMap &tmB,
+                                   const CUtensorMap &tmOut, const GemmParams &p, int grid, cudaStream_t st) {
+  switch (p.act) {
+    case GMM_ACT_NONE: return launch_gemm_act_of<GMM_ACT_NONE>(cfg, tmA, tmB, tmOut, p, grid, st);
+    case GMM_ACT_RELU: return launch_gemm_act_of<GMM_ACT_RELU>(cfg, tmA, tmB, tmOut, p, grid, st);
+    case GMM_ACT_SILU: return launch_gemm_act_of<GMM_ACT_SILU>(cfg, tmA, tmB, tmOut, p, grid, st);
+    case GMM_ACT_GELU: return launch_gemm_act_of<GMM_ACT_GELU>(cfg, tmA, tmB, tmOut, p, grid, st);
+    case GMM_ACT_GELU_TANH: return launch_gemm_act_of<GMM_ACT_GELU_TANH>(cfg, tmA, tmB, tmOut, p, grid, st);
+    case GMM_ACT_SWIGLU: return launch_gemm_act_of<GMM_ACT_SWIGLU>(cfg, tmA, tmB, tmOut, p, grid, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
 }  // namespace gmm
