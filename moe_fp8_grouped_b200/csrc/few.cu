@@ -44,11 +44,12 @@
 // Warps (512 threads, one CTA per SM): 0-1 TMA producers, 2-3 MMA issuers (2
 // owns the TMEM), 4-11 activation loaders, 12-15 epilogue (TMEM lanes 32 (w %
 // 4) ..).  Producers and issuers take alternate units: one thread's wait and
-// issue per unit bounds the stream below HBM (copies alone: 51 us against 41
-// us with two).  Each issuer sums its units of a tile in an accumulator of its
-// own; the epilogue adds the two.  A loader warp prepares every eighth unit on
-// its own, so that eight units' loads are in flight: under the weight stream
-// one takes 1000 to 2000 cycles, a unit's share of HBM 670.
+// issue per unit bounds the stream below HBM (copies alone, 235 MB: 57 and 51
+// us with one producer, 41 with two; a third gains nothing here).  Each issuer
+// sums its units of a tile in an accumulator of its own; the epilogue adds the
+// two.  A loader warp prepares every eighth unit on its own, so that eight
+// units' loads are in flight: under the weight stream one takes 1000 to 2000
+// cycles, a unit's share of HBM 670.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -64,7 +65,7 @@ constexpr int kFewThreads = 512;
 constexpr int kFewMaxSlices = 16;
 constexpr int kFewOwnTokens = 4;   // rows whose largest value every CTA finds on its own
 constexpr int kUnitBytes = 16384;  // 128 columns x 128 bytes of contraction
-constexpr int kProdWarps = 2;                // warps 0 .. 1
+constexpr int kProdWarps = 2;  // warps 0-1
 constexpr int kMmaWarp0 = 2, kMmaWarps = 2;
 constexpr int kLoadWarp0 = 4, kLoadWarps = 8;
 constexpr int kFewEpiWarp0 = 12, kFewEpiWarps = 4;
@@ -246,6 +247,10 @@ __device__ __forceinline__ void split_e4m3(const uint2 &raw, float up, uint32_t 
   const uint16_t l1 = cvt_e4m3x2((v[2] - f1.x) * 16.0f, (v[3] - f1.y) * 16.0f);
   hi = h0 | (static_cast<uint32_t>(h1) << 16);
   lo = l0 | (static_cast<uint32_t>(l1) << 16);
+}
+
+__device__ __forceinline__ float4 add4(const float4 &a, const float4 &b) {
+  return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
 }
 
 __device__ __forceinline__ float few_silu(float x) { return x / (1.0f + expf(-x)); }
@@ -643,27 +648,38 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     // one warp sums the slices of 128 columns (a tile) of one pair, four
     // columns a lane
     const int64_t cols = static_cast<int64_t>(pr.tiles) * 128;
-    auto tile4 = [&](int pair, int tile) -> float4 {
-      float4 a = __ldcg(reinterpret_cast<const float4 *>(p.partial + pair * cols + tile * 128) + lane);
+    // slice `sl` of the tile (NULL: the tile has no such slice)
+    auto part_of = [&](int pair, int tile, int sl) -> const float * {
+      if (sl == 0) return p.partial + pair * cols + tile * 128;
       const int lt = t.pair_group[pair] * pr.tiles + tile - pr.waves * static_cast<int>(gridDim.x);
-      if (lt >= 0) {
-        const float *src = p.extra + (static_cast<int64_t>(lt) * kRows + t.pos[pair] % kRows) * 128 + lane * 4;
+      if (lt < 0) return nullptr;
+      return p.extra + (static_cast<int64_t>((sl - 1) * pr.left + lt) * kRows + t.pos[pair] % kRows) * 128;
+    };
+    auto load4 = [&](const float *src) -> float4 {
+      return src ? __ldcg(reinterpret_cast<const float4 *>(src) + lane) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    };
+    auto tile4 = [&](int pair, int tile) -> float4 {
+      float4 a = load4(part_of(pair, tile, 0));
+      if (const float *src = pr.slices > 1 ? part_of(pair, tile, 1) : nullptr) {
         const int64_t step = static_cast<int64_t>(pr.left) * kRows * 128;
 #pragma unroll 4
-        for (int i = 1; i < pr.slices; ++i) {
-          const float4 b = __ldcg(reinterpret_cast<const float4 *>(src + (i - 1) * step));
-          a = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
-        }
+        for (int i = 1; i < pr.slices; ++i, src += step) a = add4(a, load4(src));
       }
       return a;
     };
+    // With few (pair, tile) items each takes a whole CTA, the warps one slice
+    // each, joined in shared memory in a fixed order (the rows' stages, idle
+    // now): one warp's loop over up to 16 slices of several terms leaves their
+    // latencies, 3 to 5 us, on a few SMs.  With many a warp takes each.
+    float4 *part = reinterpret_cast<float4 *>(sB);
+    static_assert(kSt * kBBytes >= kFewThreads * 16, "one float4 a thread");
     const int nwarps = gridDim.x * (kFewThreads / 32), w0 = warp * gridDim.x + blockIdx.x;
     if (ph == 0) {
       const int F = p.F, ft = F / 128;
-      for (int i = w0; i < p.pairs * ft; i += nwarps) {
-        const int pair = few_div(i, ft), tile = i - pair * ft, col = tile * 128 + lane * 4;
-        if (t.pair_group[pair] < 0) continue;
-        float4 g = tile4(pair, tile), u = tile4(pair, ft + tile);
+      // silu(g) * u of one pair's 128 columns (four a lane), g and u without
+      // their channel scales
+      auto activate = [&](int pair, int tile, float4 g, float4 u) {
+        const int col = tile * 128 + lane * 4;
         if constexpr (kElem == 1) {
           const float *sc = p.s1 + static_cast<int64_t>(t.ids[pair]) * 2 * F + col;
           const float4 sg = *reinterpret_cast<const float4 *>(sc), su = *reinterpret_cast<const float4 *>(sc + F);
@@ -681,6 +697,33 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
           if (lane == 0) atomicMax(p.largest + p.T + pair, m);
         }
+      };
+      if (p.pairs * ft <= 2 * static_cast<int>(gridDim.x)) {
+        for (int i = blockIdx.x; i < p.pairs * ft; i += gridDim.x) {
+          const int pair = few_div(i, ft), tile = i - pair * ft;
+          if (t.pair_group[pair] < 0) continue;
+          // warps 0-7: gate slices in turn, 8-15: up slices
+          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          for (int sl = warp % 8; sl < pr.slices; sl += 8) v = add4(v, load4(part_of(pair, tile + (warp / 8) * ft, sl)));
+          part[warp * 32 + lane] = v;
+          __syncthreads();
+          if (warp == 0) {
+            float4 u = part[8 * 32 + lane];
+#pragma unroll
+            for (int w = 1; w < 8; ++w) {
+              v = add4(v, part[w * 32 + lane]);
+              u = add4(u, part[(8 + w) * 32 + lane]);
+            }
+            activate(pair, tile, v, u);
+          }
+          __syncthreads();
+        }
+      } else {
+        for (int i = w0; i < p.pairs * ft; i += nwarps) {
+          const int pair = few_div(i, ft), tile = i - pair * ft;
+          if (t.pair_group[pair] < 0) continue;
+          activate(pair, tile, tile4(pair, tile), tile4(pair, ft + tile));
+        }
       }
       grid.sync();
       if constexpr (kElem == 1) {
@@ -689,27 +732,53 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       }
     } else {
       const int N = p.N, nt = N / 128;
-      for (int i = w0; i < p.T * nt; i += nwarps) {
-        const int tok = few_div(i, nt), tile = i - tok * nt, col = tile * 128 + lane * 4;
-        float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 2
-        for (int j = 0; j < p.k; ++j) {
-          const int pair = tok * p.k + j;
-          if (t.pair_group[pair] < 0) continue;
-          float4 v = tile4(pair, tile);
-          if constexpr (kElem == 1) {
-            const float4 s = *reinterpret_cast<const float4 *>(p.s2 + static_cast<int64_t>(t.ids[pair]) * N + col);
-            v = make_float4(v.x * s.x, v.y * s.y, v.z * s.z, v.w * s.w);
-          }
-          const float w = p.weights[pair];
-          y = make_float4(fmaf(w, v.x, y.x), fmaf(w, v.y, y.y), fmaf(w, v.z, y.z), fmaf(w, v.w, y.w));
-        }
+      auto store4 = [&](int tok, int col, const float4 &y) {
         if (p.y_f32) {
           *reinterpret_cast<float4 *>(static_cast<float *>(p.y) + static_cast<int64_t>(tok) * N + col) = y;
         } else {
           __nv_bfloat162 o[2] = {__floats2bfloat162_rn(y.x, y.y), __floats2bfloat162_rn(y.z, y.w)};
           *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.y) + static_cast<int64_t>(tok) * N + col) =
               *reinterpret_cast<uint2 *>(o);
+        }
+      };
+      auto weigh4 = [&](int pair, int col, float4 v) -> float4 {
+        if constexpr (kElem == 1) {
+          const float4 s = *reinterpret_cast<const float4 *>(p.s2 + static_cast<int64_t>(t.ids[pair]) * N + col);
+          v = make_float4(v.x * s.x, v.y * s.y, v.z * s.z, v.w * s.w);
+        }
+        const float w = p.weights[pair];
+        return make_float4(w * v.x, w * v.y, w * v.z, w * v.w);
+      };
+      if (p.T * nt <= 2 * static_cast<int>(gridDim.x)) {
+        constexpr int kWarps = kFewThreads / 32;
+        for (int i = blockIdx.x; i < p.T * nt; i += gridDim.x) {
+          const int tok = few_div(i, nt), tile = i - tok * nt, col = tile * 128 + lane * 4;
+          float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          for (int c = warp; c < p.k * pr.slices; c += kWarps) {
+            const int j = few_div(c, pr.slices), sl = c - j * pr.slices, pair = tok * p.k + j;
+            if (t.pair_group[pair] < 0) continue;
+            y = add4(y, weigh4(pair, col, load4(part_of(pair, tile, sl))));
+          }
+          part[warp * 32 + lane] = y;
+          __syncthreads();
+          if (warp == 0) {
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) y = add4(y, part[w * 32 + lane]);
+            store4(tok, col, y);
+          }
+          __syncthreads();
+        }
+      } else {
+        for (int i = w0; i < p.T * nt; i += nwarps) {
+          const int tok = few_div(i, nt), tile = i - tok * nt, col = tile * 128 + lane * 4;
+          float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 2
+          for (int j = 0; j < p.k; ++j) {
+            const int pair = tok * p.k + j;
+            if (t.pair_group[pair] < 0) continue;
+            y = add4(y, weigh4(pair, col, tile4(pair, tile)));
+          }
+          store4(tok, col, y);
         }
       }
     }
@@ -746,8 +815,9 @@ cudaError_t launch_few_inst(const CUtensorMap &tm1, const CUtensorMap &tm2, cons
   const int64_t units = static_cast<int64_t>(p.pairs) * max(p.tiles1 * p.kb1, p.tiles2 * p.kb2);
   const int grid = static_cast<int>(units < num_sms() ? units : num_sms());
   void *args[] = {const_cast<CUtensorMap *>(&tm1), const_cast<CUtensorMap *>(&tm2), const_cast<FewParams *>(&p)};
-  return cudaLaunchCooperativeKernel(reinterpret_cast<const void *>(kern), dim3(grid), dim3(kFewThreads), args,
-                                     smem, st);
+  e = cudaLaunchCooperativeKernel(reinterpret_cast<const void *>(kern), dim3(grid), dim3(kFewThreads), args, smem, st);
+  if (e != cudaSuccess) cudaGetLastError();  // reported by the return value
+  return e;
 }
 
 template <int kElem, bool kMN>

@@ -382,11 +382,11 @@ def _shape(t: torch.Tensor | None, name: str, shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
-def _scratch(ws: torch.Tensor | None, nbytes: int, device) -> torch.Tensor:
+def _scratch(ws: torch.Tensor | None, nbytes: int, like: torch.Tensor) -> torch.Tensor:
     """The caller's workspace, or one from torch's caching allocator for this
     call alone: the allocator keeps it apart per stream and per captured
     graph, so that calls on several streams or in several graphs share none."""
-    return ws if ws is not None else torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+    return ws if ws is not None else like.new_empty(max(nbytes, 256), dtype=torch.uint8)
 
 
 def gmm_fwd_act(lhs: torch.Tensor, rhs: torch.Tensor, rhs_scales: torch.Tensor | None, group_sizes: torch.Tensor,
@@ -421,15 +421,15 @@ def gmm_fwd_act(lhs: torch.Tensor, rhs: torch.Tensor, rhs_scales: torch.Tensor |
     else:
         a = _operand(_dev(lhs, "lhs", torch.bfloat16), B.DT_BF16, _dev(static_scale, "static_scale", torch.float32), r)
     if preact is None and keep_preact:
-        preact = torch.empty((M, N), dtype=torch.bfloat16, device=lhs.device)
+        preact = lhs.new_empty((M, N), dtype=torch.bfloat16)
     if out is None:
-        out = torch.empty(out_shape, dtype=out_dtype, device=lhs.device)
+        out = lhs.new_empty(out_shape, dtype=out_dtype)
     epi = B.Epilogue(a_code, _dev(bias, "bias", torch.float32),
                      _dev(residual, "residual", (torch.bfloat16, torch.float32)),
                      _TORCH_DT[residual.dtype] if residual is not None else B.DT_BF16,
                      _dev(preact, "preact", torch.bfloat16))
     with _on(lhs):
-        ws = _scratch(ws, _fwd_bytes(M, K, N, G), lhs.device)
+        ws = _scratch(ws, _fwd_bytes(M, K, N, G), lhs)
         st = B.lib().gmm_fwd_act(a, _rhs_operand(rhs, rhs_scales), int(transpose_rhs),
                                  _dev(group_sizes, "group_sizes", torch.int32), G, M, K, N, ctypes.byref(epi),
                                  _dev(out, "out", (torch.bfloat16, torch.float32)), _TORCH_DT[out.dtype],
@@ -452,11 +452,11 @@ def gmm_act_bwd(dout: torch.Tensor, preact: torch.Tensor, group_sizes: torch.Ten
     _shape(dbias, "dbias", (G, N))
     _same_device(dout, preact, group_sizes, dz, dbias, ws)
     if dz is None:
-        dz = torch.empty((M, N), dtype=torch.bfloat16, device=dout.device)
+        dz = dout.new_empty((M, N), dtype=torch.bfloat16)
     if dbias is None and with_dbias:
-        dbias = torch.empty((G, N), dtype=torch.float32, device=dout.device)
+        dbias = dout.new_empty((G, N), dtype=torch.float32)
     with _on(dout):
-        ws = _scratch(ws, _act_bwd_bytes(M, N, G), dout.device)
+        ws = _scratch(ws, _act_bwd_bytes(M, N, G), dout)
         st = B.lib().gmm_act_bwd(_dev(dout, "dout", torch.bfloat16), _dev(preact, "preact", torch.bfloat16), a_code,
                                  _dev(group_sizes, "group_sizes", torch.int32), G, M, N,
                                  _dev(dz, "dz", torch.bfloat16), _dev(dbias, "dbias", torch.float32), _dev(ws, "ws"),
@@ -492,9 +492,9 @@ def gmm_moe_few(x: torch.Tensor, expert_ids: torch.Tensor, weights: torch.Tensor
         raise ValueError(f"w1 / w2 have dtype {w1.dtype} / {w2.dtype}, expected E4M3 codes or bf16")
     dt = _TORCH_DT[w1.dtype]
     if out is None:
-        out = torch.empty((T, N), dtype=out_dtype, device=x.device)
+        out = x.new_empty((T, N), dtype=out_dtype)
     with _on(x):
-        ws = _scratch(ws, _few_bytes(T, k, G, K, F, N, dt), x.device)
+        ws = _scratch(ws, _few_bytes(T, k, G, K, F, N, dt), x)
         st = B.lib().gmm_moe_few(
             _dev(x, "x", torch.bfloat16), _dev(expert_ids, "expert_ids", torch.int32),
             _dev(weights, "weights", torch.float32), T, k,
@@ -516,8 +516,8 @@ def gmm_router_topk(logits: torch.Tensor, k: int, score: str = "softmax", select
     T, E = logits.shape
     _shape(select_bias, "select_bias", (E,))
     _same_device(logits, select_bias)
-    ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
-    weights = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+    ids = logits.new_empty((T, k), dtype=torch.int32)
+    weights = logits.new_empty((T, k), dtype=torch.float32)
     with _on(logits):
         st = B.lib().gmm_router_topk(_dev(logits, "logits", (torch.float32, torch.bfloat16)), _TORCH_DT[logits.dtype],
                                      T, E, k, _name(SCORES, score, "score"),
@@ -554,7 +554,7 @@ def gmm_combine_dweight(dy: torch.Tensor, rows: torch.Tensor, slot: torch.Tensor
     T, k = slot.shape
     _shape(dy, "dy", (T, rows.shape[1]))
     _same_device(dy, rows, slot)
-    dw = torch.empty((T, k), dtype=torch.float32, device=dy.device)
+    dw = dy.new_empty((T, k), dtype=torch.float32)
     with _on(dy):
         st = B.lib().gmm_combine_dweight(_dev(dy, "dy", torch.bfloat16), _dev(rows, "rows", torch.bfloat16),
                                          rows.shape[0], _dev(slot, "slot", torch.int32), T, k, rows.shape[1],
