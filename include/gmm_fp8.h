@@ -288,7 +288,8 @@ gmm_status gmm_act_bwd(const void *dout_bf16, const void *preact_bf16, gmm_act a
  * fp32 in an order that depends on the routing and the number of SMs only.
  * y: [T, N] of y_dtype (BF16 or F32).  With E4M3 weights a token with a value
  * that is not finite (or whose h overflows bf16) gets NaN.
- * K, F, N multiples of 128, F <= 2^19, T * k <= 1024, G <= 1024.  Every
+ * K, F, N multiples of 128, F <= 2^19, T * k <= 1024 (T == 0 is a no-op), G <=
+ * 1024.  Every
  * active expert's weights are read once per 32 of its rows (once for T <= 8):
  * for large T use gmm_fwd_swiglu, gmm_fwd and gmm_combine_rows.  The kernel is
  * a cooperative launch on every SM of the device.  Workspace:
@@ -313,7 +314,8 @@ gmm_status gmm_moe_few(const void *x_bf16, const int32_t *expert_ids, const floa
  *   weights[t, j] = scale * p_j, or with normalize scale * p_j / (sum of the
  *   chosen p), which is finite even where every chosen p underflows.
  * expert_ids: device int32 [T, k]; weights: device float [T, k].
- * E <= 1024, k <= 32, k <= E, T <= 2^24; pointers 16-byte aligned.
+ * E <= 1024, k <= 32, k <= E, T <= 2^24 (T == 0 is a no-op); pointers 16-byte
+ * aligned.
  */
 gmm_status gmm_router_topk(const void *logits, gmm_dtype logits_dtype, int64_t T, int32_t E, int32_t k,
                            gmm_score score, const float *select_bias, int normalize, float scale, int32_t *expert_ids,

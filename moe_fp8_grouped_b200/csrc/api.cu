@@ -757,7 +757,7 @@ struct FewLayout {
 };
 
 static gmm_status check_few(int64_t T, int32_t k, int32_t G, int64_t K, int64_t F, int64_t N) {
-  if (T <= 0 || k <= 0 || K <= 0 || F <= 0 || N <= 0 || G <= 0) return GMM_ERR_SHAPE;
+  if (T < 0 || k <= 0 || K <= 0 || F <= 0 || N <= 0 || G <= 0) return GMM_ERR_SHAPE;
   if (K % kBlk || F % kBlk || N % kBlk) return GMM_ERR_SHAPE;
   if (T > kFewMaxPairs || k > kFewMaxPairs || T * k > kFewMaxPairs) return GMM_ERR_UNSUPPORTED;
   if (F > (1 << 19)) return GMM_ERR_UNSUPPORTED;
@@ -849,7 +849,7 @@ gmm_status gmm_moe_few(const void *x_bf16, const int32_t *expert_ids, const floa
   g_launches = 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   gmm_status s = check_few(T, k, G, K, F, N);
-  if (s != GMM_OK) return s;
+  if (s != GMM_OK || T == 0) return s;
   if (!x_bf16 || !expert_ids || !weights || !w1.data || !w2.data || !y) return GMM_ERR_INVALID_ARG;
   if (y_dtype != GMM_BF16 && y_dtype != GMM_F32) return GMM_ERR_INVALID_ARG;
   if (w1.dtype != w2.dtype || (w1.dtype != GMM_E4M3 && w1.dtype != GMM_BF16)) return GMM_ERR_INVALID_ARG;
@@ -901,9 +901,9 @@ gmm_status gmm_moe_few(const void *x_bf16, const int32_t *expert_ids, const floa
 }
 
 static gmm_status check_router(const void *logits, gmm_dtype dtype, int64_t T, int32_t E, int32_t k, gmm_score score) {
-  if (T <= 0 || E <= 0 || k <= 0 || k > E) return GMM_ERR_SHAPE;
+  if (T < 0 || E <= 0 || k <= 0 || k > E) return GMM_ERR_SHAPE;
   if (T > (1 << 24) || E > kMaxGroups || k > 32) return GMM_ERR_UNSUPPORTED;
-  if (!logits || (dtype != GMM_F32 && dtype != GMM_BF16)) return GMM_ERR_INVALID_ARG;
+  if ((!logits && T) || (dtype != GMM_F32 && dtype != GMM_BF16)) return GMM_ERR_INVALID_ARG;
   if (score != GMM_SCORE_SOFTMAX && score != GMM_SCORE_SIGMOID) return GMM_ERR_INVALID_ARG;
   return GMM_OK;
 }
@@ -913,7 +913,7 @@ gmm_status gmm_router_topk(const void *logits, gmm_dtype logits_dtype, int64_t T
                            float *weights, void *stream) {
   g_launches = 0;
   gmm_status s = check_router(logits, logits_dtype, T, E, k, score);
-  if (s != GMM_OK) return s;
+  if (s != GMM_OK || T == 0) return s;
   if (!expert_ids || !weights) return GMM_ERR_INVALID_ARG;
   if (!al16(logits) || !al16(expert_ids) || !al16(weights) || (select_bias && !al16(select_bias)))
     return GMM_ERR_ALIGNMENT;
@@ -940,7 +940,7 @@ gmm_status gmm_router_topk_bwd(const float *dweights, const void *logits, gmm_dt
                                int normalize, float scale, void *dlogits, void *stream) {
   g_launches = 0;
   gmm_status s = check_router(logits, logits_dtype, T, E, k, score);
-  if (s != GMM_OK) return s;
+  if (s != GMM_OK || T == 0) return s;
   if (!dweights || !expert_ids || !dlogits) return GMM_ERR_INVALID_ARG;
   if (!al16(logits) || !al16(expert_ids) || !al16(dweights) || !al16(dlogits)) return GMM_ERR_ALIGNMENT;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

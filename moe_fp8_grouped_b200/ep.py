@@ -195,7 +195,7 @@ def combine_rows(rows: torch.Tensor, slot: torch.Tensor, weight: torch.Tensor, o
 
 def ep_moe_fwd(x_codes: torch.Tensor, static_scale: torch.Tensor, expert_ids: torch.Tensor,
                weights: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor, group=None,
-               out_dtype=torch.bfloat16, validate: bool = True) -> torch.Tensor:
+               out_dtype=torch.bfloat16, validate: bool = True, keep_rows: bool = False):
     """One expert-parallel expert projection for this rank's T tokens.
 
     x_codes: E4M3 codes [T, K] of the tokens (static rule, ``static_scale``
@@ -204,6 +204,9 @@ def ep_moe_fwd(x_codes: torch.Tensor, static_scale: torch.Tensor, expert_ids: to
     y [T, N] = sum_j weights[t, j] * (x[t] @ W[expert_ids[t, j]]).
     On one rank with validate=False nothing synchronizes with the host, so
     the call can be captured in a CUDA graph (see EPForwardGraph).
+    keep_rows=True returns (y, h, slot): the experts' output rows h [T*k, N] as
+    they came back and slot [T, k] (int32), the row of each choice, from which
+    gmm_combine_dweight(dy, h, slot) gives the routing weights' gradient.
     """
     P = dist.get_world_size(group) if dist.is_initialized() else 1
     El, K, N = w_codes.shape
@@ -232,7 +235,9 @@ def ep_moe_fwd(x_codes: torch.Tensor, static_scale: torch.Tensor, expert_ids: to
         h = exchange_rows(gather_rows(h, inv), arrive, rt.send_splits, group)
     # h[i] is the result of flat position order[i]; slot of (t, j) = i
     slot = torch.empty_like(order).scatter_(0, order, torch.arange(order.numel(), device=order.device))
-    return combine_rows(h, slot.view(T, k), weights, out_dtype)
+    slot = slot.view(T, k).to(torch.int32)
+    y = combine_rows(h, slot, weights, out_dtype)
+    return (y, h, slot) if keep_rows else y
 
 
 class EPForwardGraph:
@@ -273,7 +278,8 @@ def ep_moe_bwd(x_codes: torch.Tensor, static_scale: torch.Tensor, expert_ids: to
     together with the forward's E4M3 codes of x[t]; there gmm_backward (dout
     quantized once) gives dlhs rows and dW; the dlhs rows return and are
     summed per token: dx[t] = sum_j dlhs_{t, j}.  The routing weights'
-    gradient (dy . h) belongs to the router and is not computed here.
+    gradient (dy . h) is gmm_combine_dweight of the rows that ep_moe_fwd keeps
+    (keep_rows); gmm_router_topk_bwd takes it on to the router's logits.
     """
     P = dist.get_world_size(group) if dist.is_initialized() else 1
     El, K, N = w_codes.shape

@@ -69,7 +69,8 @@ def test_moe_few(L):
              ws=FAKE, nbytes=BIG):
         return L.gmm_moe_few(x, ids, wts, T, k, w1 or op(), w2 or op(), 0, G, K, F, N, y, ydt, ws, nbytes, None)
 
-    assert call(T=0) == SHAPE and call(k=0) == SHAPE and call(G=0) == SHAPE
+    assert call(T=-1) == SHAPE and call(k=0) == SHAPE and call(G=0) == SHAPE
+    assert call(T=0) == 0  # nothing to do
     assert call(K=200) == SHAPE and call(F=64) == SHAPE and call(N=100) == SHAPE
     assert call(T=513, k=2) == UNSUPPORTED and call(T=2 ** 40, k=2 ** 30) == UNSUPPORTED
     assert call(G=1025) == UNSUPPORTED and call(F=(1 << 19) + 128) == UNSUPPORTED
@@ -93,7 +94,8 @@ def test_router(L):
     def call(x=FAKE, dt=B.DT_F32, T=4, E=8, k=2, score=B.SCORE_SOFTMAX, bias=None, ids=FAKE, w=FAKE):
         return L.gmm_router_topk(x, dt, T, E, k, score, bias, 0, 1.0, ids, w, None)
 
-    assert call(T=0) == SHAPE and call(E=0) == SHAPE and call(k=0) == SHAPE and call(k=9) == SHAPE
+    assert call(T=-1) == SHAPE and call(E=0) == SHAPE and call(k=0) == SHAPE and call(k=9) == SHAPE
+    assert call(T=0) == 0 and call(T=0, x=None, ids=None, w=None) == 0  # nothing to do
     assert call(E=1025) == UNSUPPORTED and call(E=64, k=33) == UNSUPPORTED and call(T=(1 << 24) + 1) == UNSUPPORTED
     assert call(x=None) == INVALID and call(dt=B.DT_E4M3) == INVALID and call(score=2) == INVALID
     assert call(ids=None) == INVALID and call(w=None) == INVALID
@@ -102,6 +104,7 @@ def test_router(L):
     def bwd(dw=FAKE, x=FAKE, ids=FAKE, dl=FAKE, T=4, E=8, k=2):
         return L.gmm_router_topk_bwd(dw, x, B.DT_BF16, ids, T, E, k, B.SCORE_SIGMOID, 1, 1.0, dl, None)
 
+    assert bwd(T=0) == 0
     assert bwd(k=9) == SHAPE and bwd(dw=None) == INVALID and bwd(ids=None) == INVALID and bwd(dl=None) == INVALID
     assert bwd(dl=FAKE + 2) == ALIGN
 

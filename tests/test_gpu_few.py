@@ -249,3 +249,59 @@ def test_device_status_is_clean():
     y = gm.gmm_moe_few(x, ids, wts, *w, ws=ws)
     assert gm.gmm_read_device_status(ws) == (0, 0)
     assert torch.equal(y, gm.gmm_moe_few(x, ids, wts, *w))
+
+
+def test_thousand_experts_and_single_ones():
+    T, k, G, K, F, N = 6, 5, 1000, 128, 128, 128
+    w, d1, d2 = _layer(G, K, F, N, "e4m3", False)
+    x, ids, wts = _inputs(T, k, G, K, seed=4)
+    ids[0, 0], ids[1, 0] = 0, G - 1
+    y = gm.gmm_moe_few(x, ids, wts, *w, out_dtype=torch.float32)
+    ref, bound = _ref(x, ids, wts, d1, d2)
+    _check(y, ref, bound, "G = 1000")
+
+
+@pytest.mark.parametrize("T,k", [(40, 2), (1, 32)])
+def test_many_tokens_share_row_maxima_and_one_token_many_choices(T, k):
+    G, K, F, N = 3, 1152, 256, 384  # 1152: a row of more than one piece, the last one short
+    w, d1, d2 = _layer(G, K, F, N, "e4m3", True)
+    x, ids, wts = _inputs(T, k, G, K, seed=8, distinct=False)
+    x[0] *= 1e4
+    x[-1, -1] = 250.0  # the largest value in the short piece
+    y = gm.gmm_moe_few(x, ids, wts, *w, transpose_rhs=True, out_dtype=torch.float32)
+    ref, bound = _ref(x, ids, wts, d1, d2)
+    _check(y, ref, bound, f"T={T} k={k}")
+
+
+def test_bf16_weights_take_any_value():
+    T, k, G, K, F, N = 3, 1, 2, 256, 128, 128
+    w, d1, d2 = _layer(G, K, F, N, "bf16", False)
+    x, ids, wts = _inputs(T, k, G, K, seed=9)
+    x[0] *= 1e-20
+    x[1, 5] = 1e6
+    x[2, 9] = float("inf")
+    y = gm.gmm_moe_few(x, ids, wts, *w, out_dtype=torch.float32)
+    ref, bound = _ref(x[:2], ids[:2], wts[:2], d1, d2)
+    _check(y[:2], ref, bound + 1e-30, "bf16")
+    assert not bool(torch.isfinite(y[2]).all())
+
+
+def test_no_tokens():
+    w, _, _ = _layer(2, 128, 128, 256, "e4m3", False)
+    y = gm.gmm_moe_few(torch.empty(0, 128, dtype=torch.bfloat16, device=DEV),
+                       torch.empty(0, 2, dtype=torch.int32, device=DEV), torch.empty(0, 2, device=DEV), *w)
+    assert y.shape == (0, 256)
+
+
+def test_results_do_not_depend_on_the_other_tokens():
+    """A token's row is the same whatever else is in the batch, up to the order
+    of the sums (which depends on the routing): 2e-3 * A of the bound is far
+    above it; tokens that choose no expert change nothing at all."""
+    T, k, G, K, F, N = 6, 2, 4, 512, 256, 256
+    w, d1, d2 = _layer(G, K, F, N, "e4m3", False)
+    x, ids, wts = _inputs(T, k, G, K, seed=10)
+    alone = gm.gmm_moe_few(x, ids, wts, *w, out_dtype=torch.float32)
+    pad_x = torch.cat([x, torch.randn(2, K, device=DEV).bfloat16()])
+    pad_ids = torch.cat([ids, torch.full((2, k), -1, dtype=torch.int32, device=DEV)])
+    padded = gm.gmm_moe_few(pad_x, pad_ids, torch.cat([wts, wts[:2]]), *w, out_dtype=torch.float32)
+    assert torch.equal(padded[:T], alone) and bool((padded[T:] == 0).all())
