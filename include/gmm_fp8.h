@@ -288,13 +288,14 @@ gmm_status gmm_act_bwd(const void *dout_bf16, const void *preact_bf16, gmm_act a
  * fp32 in an order that depends on the routing and the number of SMs only.
  * y: [T, N] of y_dtype (BF16 or F32).  With E4M3 weights a token with a value
  * that is not finite (or whose h overflows bf16) gets NaN.
- * K, F, N multiples of 128, F <= 2^19, T * k <= 1024 (T == 0 is a no-op), G <=
- * 1024.  Every
- * active expert's weights are read once per 32 of its rows (once for T <= 8):
- * for large T use gmm_fwd_swiglu, gmm_fwd and gmm_combine_rows.  The kernel is
- * a cooperative launch on every SM of the device.  Workspace:
- * gmm_moe_few_workspace_bytes (0 for invalid sizes), read and written within
- * the call; calls that may overlap need workspaces of their own.
+ * K, F, N multiples of 128, F <= 2^19, T * k <= 1024 (T == 0 is a no-op),
+ * G <= 1024.  Every active expert's weights are read once per 32 of its rows:
+ * for large T use gmm_fwd_swiglu, gmm_fwd and gmm_combine_rows.  With E4M3
+ * weights a row's values below 2^-13 of its largest keep an absolute error of
+ * 2^-22 of that largest.  The kernel is a cooperative launch on every SM of
+ * the device.  Workspace: gmm_moe_few_workspace_bytes (0 for invalid sizes),
+ * read and written within the call; calls that may overlap need workspaces of
+ * their own.
  */
 size_t gmm_moe_few_workspace_bytes(int64_t T, int32_t k, int32_t G, int64_t K, int64_t F, int64_t N,
                                    gmm_dtype weight_dtype);

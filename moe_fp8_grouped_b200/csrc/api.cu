@@ -774,7 +774,7 @@ static FewLayout few_layout(int64_t T, int32_t k, int64_t F, int64_t N) {
   L.largest = L.h + align256(static_cast<size_t>(pairs) * F * 2);
   L.partial = L.largest + align256(sizeof(uint32_t) * static_cast<size_t>(T + pairs));
   L.extra = L.partial + align256(sizeof(float) * static_cast<size_t>(pairs) * cols);
-  L.total = L.extra + align256(sizeof(float) * few_extra_floats(T));
+  L.total = L.extra + align256(sizeof(float) * few_extra_floats());
   return L;
 }
 

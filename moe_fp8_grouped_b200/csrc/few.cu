@@ -21,8 +21,7 @@
 // Tile.  The weights are the 128-row operand of tcgen05.mma and stay in the
 // layout they have in memory (MN-major for [G, K, N], K-major for [G, N, K]):
 // TMA brings them to shared memory and no register ever holds one.  The
-// expert's rows (at most kRows a group; an expert with more gets several
-// groups) are the MMA's columns.
+// expert's rows are the MMA's columns.
 //
 // Activations stay bf16 in precision although the MMA multiplies E4M3: a bf16
 // value has 8 significant bits, so scaled by a power of two (one per row, that
@@ -31,15 +30,18 @@
 // the row's largest and within 2^-22 of that largest below.  hi and lo are
 // separate MMA columns, joined and unscaled once per tile.  (A scale per block
 // of 128 instead would need every block's accumulator read and scaled on its
-// own: measured, that epilogue took 500 to 1000 cycles a unit and was the
-// bound.)  bf16 weights multiply
-// the bf16 rows as they are.
+// own: that epilogue took 500 to 1000 cycles a unit and was the bound.)  bf16
+// weights multiply the bf16 rows as they are.
 //
 // The layer is one cooperative launch: gate|up product, grid barrier, SwiGLU
 // of the summed partials (rounded to bf16, as the separate calls round it),
 // grid barrier, down product, grid barrier, weighted sum.  The producer starts
 // the down product's first copies before the barriers, so HBM keeps working
-// across them.
+// across them.  Measured (us): one token, two of 8 experts, K = 4096, F = 14336
+// E4M3: 70, of which 53.7 is the weights at the copy rate; 16 tokens, 8 of 256
+// experts each, K = 7168, F = 2048: 645 to 675 (684 for the expected experts);
+// the smallest layers 16 (set-up 2.4, a barrier 1.2, two chains of load,
+// multiply and sum).
 //
 // Warps (512 threads, one CTA per SM): 0-1 TMA producers, 2-3 MMA issuers (2
 // owns the TMEM), 4-11 activation loaders, 12-15 epilogue (TMEM lanes 32 (w %
@@ -63,27 +65,26 @@ namespace {
 
 constexpr int kFewThreads = 512;
 constexpr int kFewMaxSlices = 16;
-constexpr int kFewOwnTokens = 4;   // rows whose largest value every CTA finds on its own
+// Tokens whose largest magnitudes every CTA finds on its own; more are shared
+// through memory and one more barrier (2 us; 16 tokens of 7168 values took the
+// same 625 to 627 us either way, four tokens 120.1 on their own, 121.5 shared).
+constexpr int kFewOwnTokens = 30;
 constexpr int kUnitBytes = 16384;  // 128 columns x 128 bytes of contraction
-constexpr int kProdWarps = 2;  // warps 0-1
+constexpr int kProdWarps = 2;      // warps 0-1
 constexpr int kMmaWarp0 = 2, kMmaWarps = 2;
 constexpr int kLoadWarp0 = 4, kLoadWarps = 8;
 constexpr int kFewEpiWarp0 = 12, kFewEpiWarps = 4;
 
-// stages and tile accumulators in flight of the two variants
-template <int kRows>
-struct FewCfg;
-template <>
-struct FewCfg<8> {
-  static constexpr int kStages = 10, kBufs = 4;
-};
-template <>
-struct FewCfg<32> {
-  static constexpr int kStages = 8, kBufs = 2;
-};
-
-template <int kRows>
-constexpr int few_b_bytes() { return 2 * kRows * 128; }  // hi rows and lo rows
+// Rows of a group: an expert with more takes several groups, each of which
+// reads its weights (a variant of 8 rows with 10 stages ran no faster for 1 to
+// 8 tokens: 71.4 against 70.7 us for one, 199.9 against 199.2 for eight of the
+// Mixtral-like layer).
+constexpr int kRows = 32;
+constexpr int kSt = 8, kBufs = 2;             // stages; tile accumulators in flight
+constexpr int kBBytes = 2 * kRows * 128;      // a stage's rows: hi and lo
+constexpr int kBufCols = 2 * kRows;           // TMEM columns of one issuer's accumulator
+constexpr int kTmem = kBufs * kMmaWarps * kBufCols;
+static_assert((kTmem & (kTmem - 1)) == 0 && kTmem >= 32 && kTmem <= 512, "TMEM columns: a power of two");
 
 // a / b for 0 <= a < 2^24, b > 0: the set-up and the tile switches divide by
 // sizes known only at run time, and the code of exact integer divisions cost
@@ -169,16 +170,14 @@ struct Cursor {
 };
 
 // shared memory behind the stages
-template <int kRows>
 struct FewTail {
-  using C = FewCfg<kRows>;
   // stage s: weights landed; weights landed and rows written; MMAs done
-  uint64_t full_a[C::kStages], full[C::kStages], done[C::kStages];
+  uint64_t full_a[kSt], full[kSt], done[kSt];
   // accumulator b: sums of issuer i complete
-  uint64_t tfull[C::kBufs][kMmaWarps];
+  uint64_t tfull[kBufs][kMmaWarps];
   uint64_t drain[kMmaWarps];
-  uint64_t tempty[C::kBufs];  // accumulator b: read (the only barrier with more than one arrival)
-  int last[C::kStages];       // the stage's newest copy (unit), -1: none
+  uint64_t tempty[kBufs];  // accumulator b: read (the only barrier with more than one arrival)
+  int last[kSt];       // the stage's newest copy (unit), -1: none
   uint32_t tmem_slot;
   int abort_flag, no_abort;
   Product prod[2];
@@ -195,11 +194,8 @@ struct FewTail {
   int ids[kFewMaxPairs];
 };
 
-template <int kRows>
-constexpr size_t few_smem_bytes() {
-  return 1024 + static_cast<size_t>(FewCfg<kRows>::kStages) * (kUnitBytes + few_b_bytes<kRows>()) +
-         sizeof(FewTail<kRows>);
-}
+constexpr size_t kFewSmem = 1024 + static_cast<size_t>(kSt) * (kUnitBytes + kBBytes) + sizeof(FewTail);
+static_assert(kFewSmem <= 232448, "shared memory of one CTA");
 
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&v)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -255,23 +251,16 @@ __device__ __forceinline__ float4 add4(const float4 &a, const float4 &b) {
 
 __device__ __forceinline__ float few_silu(float x) { return x / (1.0f + expf(-x)); }
 
-template <int kElem, bool kMN, int kRows>
+template <int kElem, bool kMN>
 __global__ void __launch_bounds__(kFewThreads, 1)
     moe_few_kernel(const __grid_constant__ CUtensorMap tm1, const __grid_constant__ CUtensorMap tm2,
                    const FewParams p) {
-  using C = FewCfg<kRows>;
-  using Tail = FewTail<kRows>;
-  constexpr int kSt = C::kStages, kBufs = C::kBufs;
-  constexpr int kBBytes = few_b_bytes<kRows>();
   constexpr int kBKe = 128 / kElem;  // contraction elements per unit
-  constexpr int kBufCols = 2 * kRows;  // columns of one issuer's accumulator
-  constexpr int kTmem = kBufs * kMmaWarps * kBufCols;
-  static_assert((kTmem & (kTmem - 1)) == 0 && kTmem >= 32 && kTmem <= 512, "TMEM columns: a power of two");
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *sA = smem, *sB = smem + kSt * kUnitBytes;
-  Tail &t = *reinterpret_cast<Tail *>(sB + kSt * kBBytes);
+  FewTail &t = *reinterpret_cast<FewTail *>(sB + kSt * kBBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   cooperative_groups::grid_group grid = cooperative_groups::this_grid();
 
@@ -545,10 +534,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         }
         const int cnt = t.g_count[c.group], lo_row = (cnt + 7) & ~7, f = t.g_first[c.group];
         uint8_t *b = sB + s * kBBytes;
-        for (int r0 = 0; r0 < kRows; r0 += 8) {
-          if (kRows > 8 && r0 >= cnt) break;
+#pragma unroll 1  // 32 rows unrolled overran the instruction cache
+        for (int r0 = 0; r0 < cnt; r0 += 8) {
           uint2 next[8];
-          if (kRows > 8 && r0 + 8 < cnt) fetch(next, r0 + 8);
+          if (r0 + 8 < cnt) fetch(next, r0 + 8);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             if (r0 + i < cnt) {
@@ -564,9 +553,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
               }
             }
           }
-          if (kRows > 8)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) raw[i] = next[i];
+          for (int i = 0; i < 8; ++i) raw[i] = next[i];
         }
         fence_async_smem();
         __syncwarp();
@@ -670,7 +658,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     // With few (pair, tile) items each takes a whole CTA, the warps one slice
     // each, joined in shared memory in a fixed order (the rows' stages, idle
     // now): one warp's loop over up to 16 slices of several terms leaves their
-    // latencies, 3 to 5 us, on a few SMs.  With many a warp takes each.
+    // latencies, 3 to 5 us, on a few SMs (one Mixtral-like token 74.5 us by
+    // warps, 71.2 so).  With more than two a CTA, a warp takes each (the same
+    // within 1 % up to 32 tokens).
     float4 *part = reinterpret_cast<float4 *>(sB);
     static_assert(kSt * kBBytes >= kFewThreads * 16, "one float4 a thread");
     const int nwarps = gridDim.x * (kFewThreads / 32), w0 = warp * gridDim.x + blockIdx.x;
@@ -704,7 +694,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           if (t.pair_group[pair] < 0) continue;
           // warps 0-7: gate slices in turn, 8-15: up slices
           float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          for (int sl = warp % 8; sl < pr.slices; sl += 8) v = add4(v, load4(part_of(pair, tile + (warp / 8) * ft, sl)));
+          for (int sl = warp % 8; sl < pr.slices; sl += 8)
+            v = add4(v, load4(part_of(pair, tile + (warp / 8) * ft, sl)));
           part[warp * 32 + lane] = v;
           __syncthreads();
           if (warp == 0) {
@@ -804,39 +795,33 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   }
 }
 
-template <int kElem, bool kMN, int kRows>
+template <int kElem, bool kMN>
 cudaError_t launch_few_inst(const CUtensorMap &tm1, const CUtensorMap &tm2, const FewParams &p, cudaStream_t st) {
-  auto kern = moe_few_kernel<kElem, kMN, kRows>;
-  constexpr size_t smem = few_smem_bytes<kRows>();
-  static_assert(smem <= 232448, "shared memory of one CTA");
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  auto kern = moe_few_kernel<kElem, kMN>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kFewSmem));
   if (e != cudaSuccess) return e;
   // no more CTAs than units: the barriers of a small layer span fewer SMs
   const int64_t units = static_cast<int64_t>(p.pairs) * max(p.tiles1 * p.kb1, p.tiles2 * p.kb2);
   const int grid = static_cast<int>(units < num_sms() ? units : num_sms());
   void *args[] = {const_cast<CUtensorMap *>(&tm1), const_cast<CUtensorMap *>(&tm2), const_cast<FewParams *>(&p)};
-  e = cudaLaunchCooperativeKernel(reinterpret_cast<const void *>(kern), dim3(grid), dim3(kFewThreads), args, smem, st);
+  e = cudaLaunchCooperativeKernel(reinterpret_cast<const void *>(kern), dim3(grid), dim3(kFewThreads), args, kFewSmem,
+                                  st);
   if (e != cudaSuccess) cudaGetLastError();  // reported by the return value
   return e;
 }
 
-template <int kElem, bool kMN>
-cudaError_t launch_few_rows(const CUtensorMap &tm1, const CUtensorMap &tm2, const FewParams &p, cudaStream_t st) {
-  return p.T <= 8 ? launch_few_inst<kElem, kMN, 8>(tm1, tm2, p, st)
-                  : launch_few_inst<kElem, kMN, 32>(tm1, tm2, p, st);
-}
-
 }  // namespace
 
-size_t few_extra_floats(int64_t T) {
+size_t few_extra_floats() {
   // tiles left over (fewer than CTAs) x (slices - 1) x rows of a group x 128
-  return static_cast<size_t>(num_sms()) * (kFewMaxSlices - 1) * (T <= 8 ? 8 : 32) * 128;
+  return static_cast<size_t>(num_sms()) * (kFewMaxSlices - 1) * kRows * 128;
 }
 
 cudaError_t launch_moe_few(int elem, bool mn_major, const CUtensorMap &tm1, const CUtensorMap &tm2,
                            const FewParams &p, cudaStream_t st) {
-  if (elem == 1) return mn_major ? launch_few_rows<1, true>(tm1, tm2, p, st) : launch_few_rows<1, false>(tm1, tm2, p, st);
-  return mn_major ? launch_few_rows<2, true>(tm1, tm2, p, st) : launch_few_rows<2, false>(tm1, tm2, p, st);
+  if (elem == 1)
+    return mn_major ? launch_few_inst<1, true>(tm1, tm2, p, st) : launch_few_inst<1, false>(tm1, tm2, p, st);
+  return mn_major ? launch_few_inst<2, true>(tm1, tm2, p, st) : launch_few_inst<2, false>(tm1, tm2, p, st);
 }
 
 }  // namespace gmm

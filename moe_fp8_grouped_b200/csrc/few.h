@@ -28,8 +28,8 @@ struct FewParams {
   uint64_t wait_limit_ns;
 };
 
-// Floats of FewParams::extra for T tokens.
-size_t few_extra_floats(int64_t T);
+// Floats of FewParams::extra.
+size_t few_extra_floats();
 
 cudaError_t launch_moe_few(int elem, bool mn_major, const CUtensorMap &tm1, const CUtensorMap &tm2,
                            const FewParams &p, cudaStream_t st);
