@@ -246,7 +246,10 @@ typedef struct {
  * Forward gmm with bias, activation and residual in its epilogue:
  *   z[m, :]   = gmm_fwd(lhs, rhs)[m, :] + bias[g(m), :]
  *   out[m, :] = act(z[m, :]) + residual[m, :]
- * With G = 1 this is a dense product.  lhs, rhs, rules, layouts, group_sizes
+ * With G = 1 this is a dense product.  A bf16 lhs with the dynamic rule gets
+ * the block scales fl32(amax * fl32(1/448)), as torch divides a tensor by a
+ * constant; gmm_fwd and gmm_quantize divide, at most one ulp away, so codes
+ * that fall between two E4M3 values may differ.  All else of lhs, rhs, rules, layouts, group_sizes
  * and the workspace (gmm_workspace_bytes(GMM_OP_FWD, M, K, N, G)) are
  * gmm_fwd's; z, the activation and the sum are fp32, rounded once to out and
  * (on its own) to preact.  Nout = N, or N / 2 for GMM_ACT_SWIGLU, which takes

@@ -396,8 +396,7 @@ static gmm_status fwd_impl(gmm_operand lhs, gmm_operand rhs, int transpose_rhs, 
   const WsLayout L = ws_layout(GMM_OP_FWD, M, K, N, G);
   if (!ws || ws_bytes < L.total) return GMM_ERR_WORKSPACE;
   WsPtrs P = carve(ws, L);
-  if ((s = cuda_status(prof("plan", st, [&] { return launch_plan(group_sizes, G, M, P.offs, P.tpre, P.status, st); }))) != GMM_OK) return s;
-  int n = 1;
+  int n = 0;
   const bool dyn = lhs.rule == GMM_Q_DYNAMIC;
   const bool preq = lhs.dtype == GMM_E4M3;  // codes and scales supplied by the caller
   const bool blk = elem == 1 && rhs.rule == GMM_Q_DYNAMIC;  // block-wise rhs scales [G, K/128, N]
@@ -405,15 +404,28 @@ static gmm_status fwd_impl(gmm_operand lhs, gmm_operand rhs, int transpose_rhs, 
   const void *A = lhs.data;
   uint8_t *codes = codes_out ? codes_out : P.codes_a;
   float *qscales = (codes_out && dyn) ? scales_out : P.scales_a;
-  if (elem == 1 && !preq) {
-    s = cuda_status(prof("quant_rows", st, [&] {
-      return launch_quant_rows(lhs.data, M, K, dyn, dyn ? nullptr : lhs.scale, nullptr, P.offs, G, codes, qscales,
-                               P.status, st);
+  const bool quantize = elem == 1 && !preq;
+  const float *static_scale = dyn ? nullptr : lhs.scale;
+  if (epi && quantize) {  // one launch for both (the small products are bound by launches)
+    s = cuda_status(prof("plan_quant_rows", st, [&] {
+      return launch_plan_quant_rows(group_sizes, G, M, P.offs, P.tpre, lhs.data, K, dyn, static_scale, codes, qscales,
+                                    P.status, st);
     }));
     if (s != GMM_OK) return s;
     ++n;
-    A = codes;
+  } else {
+    s = cuda_status(prof("plan", st, [&] { return launch_plan(group_sizes, G, M, P.offs, P.tpre, P.status, st); }));
+    if (s != GMM_OK) return s;
+    ++n;
+    if (quantize) {
+      s = cuda_status(prof("quant_rows", st, [&] {
+        return launch_quant_rows(lhs.data, M, K, dyn, static_scale, nullptr, P.offs, G, codes, qscales, P.status, st);
+      }));
+      if (s != GMM_OK) return s;
+      ++n;
+    }
   }
+  if (quantize) A = codes;
   const bool bmn = transpose_rhs == 0;  // [G, K, N]: N contiguous = MN-major B
   const uint32_t bke = 128 / elem;
   // (a promoted product with a fused epilogue has no pair tiles)

@@ -48,6 +48,12 @@ cudaError_t launch_quant_rows(const void *x, int64_t rows, int64_t cols, bool dy
                               const float *col_scale, const int *offs, int G, uint8_t *codes, float *scales,
                               uint32_t *status, cudaStream_t st);
 
+// launch_plan and launch_quant_rows (no column scale; dynamic scales by a
+// product with 1/448) in one launch.
+cudaError_t launch_plan_quant_rows(const int32_t *sizes, int G, int64_t M, int *offs, int *tpre, const void *x,
+                                   int64_t cols, bool dynamic, const float *static_scale, uint8_t *codes,
+                                   float *scales, uint32_t *status, cudaStream_t st);
+
 // Chunk quantizer (axis 0, tgmm operand), transposed + padded codes.
 // bf16_copy: write the bf16 values instead of codes (bf16 family packing).
 cudaError_t launch_quant_chunks(const void *x, int64_t rows, int64_t cols, bool dynamic, const float *static_scale,

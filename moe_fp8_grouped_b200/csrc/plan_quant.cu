@@ -20,8 +20,9 @@ namespace gmm {
 // One warp.  Lane l owns groups [l*per, (l+1)*per).  Negative sizes count as
 // 0; group g spans rows [min(P_g, M), min(P_g + s_g, M)) with P the prefix of
 // the non-negative sizes.  tpre is the prefix of ceil(rows / 128).
-__global__ void plan_kernel(const int32_t *__restrict__ sizes, int G, int64_t M, int *__restrict__ offs,
-                            int *__restrict__ tpre, uint32_t *__restrict__ status) {
+__device__ __forceinline__ void plan_groups(const int32_t *__restrict__ sizes, int G, int64_t M,
+                                            int *__restrict__ offs, int *__restrict__ tpre,
+                                            uint32_t *__restrict__ status) {
   const int lane = threadIdx.x;
   const int per = (G + 31) / 32;
   const int g0 = min(G, lane * per), g1 = min(G, g0 + per);
@@ -69,6 +70,11 @@ __global__ void plan_kernel(const int32_t *__restrict__ sizes, int G, int64_t M,
   if (lane == 0) *status = (bad || total > M) ? GMM_DEV_GROUP_SIZES : 0u;
 }
 
+__global__ void plan_kernel(const int32_t *__restrict__ sizes, int G, int64_t M, int *__restrict__ offs,
+                            int *__restrict__ tpre, uint32_t *__restrict__ status) {
+  plan_groups(sizes, G, M, offs, tpre, status);
+}
+
 cudaError_t launch_plan(const int32_t *sizes, int G, int64_t M, int *offs, int *tpre, uint32_t *status,
                         cudaStream_t st) {
   plan_kernel<<<1, 32, 0, st>>>(sizes, G, M, offs, tpre, status);
@@ -81,8 +87,10 @@ __device__ __forceinline__ bool static_scale_ok(float s) { return isfinite(s) &&
 
 // Dynamic scale of a block: s = fl32(amax / 448), inv = fl32(1 / s), both 0
 // when s is 0 or when 1/s overflows.
+// kTimes: s = fl32(amax * fl32(1 / 448)) instead, at most one ulp away.
+template <bool kTimes = false>
 __device__ __forceinline__ void dyn_scale(float amax, float &s, float &inv) {
-  s = __fdiv_rn(amax, 448.0f);
+  s = kTimes ? __fmul_rn(amax, 1.0f / 448.0f) : __fdiv_rn(amax, 448.0f);
   inv = (s == 0.0f) ? 0.0f : __fdiv_rn(1.0f, s);
   if (isinf(inv)) {
     s = 0.0f;
@@ -119,13 +127,12 @@ __device__ __forceinline__ void bf16x8_to_f32(const uint4 &u, float (&v)[8]) {
 // bytes) and kSegs segments per step, all loads issued first.
 constexpr int kSegs = 4;
 
-template <bool kDynamic, bool kColMult>
-__global__ void __launch_bounds__(256) quant_rows_kernel(const __nv_bfloat16 *__restrict__ x, int64_t rows,
-                                                         int64_t cols, const float *__restrict__ static_scale,
-                                                         const float *__restrict__ col_scale,
-                                                         const int *__restrict__ offs, int G,
-                                                         uint8_t *__restrict__ codes, float *__restrict__ scales,
-                                                         uint32_t *__restrict__ status) {
+template <bool kDynamic, bool kColMult, bool kTimes = false>
+__device__ __forceinline__ void quant_rows_of(int64_t block, int64_t nblocks, const __nv_bfloat16 *__restrict__ x,
+                                              int64_t rows, int64_t cols, const float *__restrict__ static_scale,
+                                              const float *__restrict__ col_scale, const int *__restrict__ offs, int G,
+                                              uint8_t *__restrict__ codes, float *__restrict__ scales,
+                                              uint32_t *__restrict__ status) {
   __shared__ int s_offs[kMaxGroups + 1];
   if constexpr (kColMult) {
     for (int i = threadIdx.x; i <= G; i += blockDim.x) s_offs[i] = offs[i];
@@ -136,13 +143,13 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const __nv_bfloat16 *__
     const float s = *static_scale;
     const bool ok = static_scale_ok(s);
     inv_static = ok ? __fdiv_rn(1.0f, s) : 0.0f;
-    if (!ok && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(status, GMM_DEV_SCALE);
+    if (!ok && block == 0 && threadIdx.x == 0) atomicOr(status, GMM_DEV_SCALE);
   }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int half = lane >> 4, hl = lane & 15;
   const int segs_per_row = static_cast<int>((cols + 255) / 256);
-  const int64_t nwarps = static_cast<int64_t>(gridDim.x) * 8;
-  for (int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + warp; r < rows; r += nwarps) {
+  const int64_t nwarps = nblocks * 8;
+  for (int64_t r = block * 8 + warp; r < rows; r += nwarps) {
     const __nv_bfloat16 *xr = x + r * cols;
     uint8_t *cr = codes + r * cols;
     const float *csr = nullptr;
@@ -195,7 +202,7 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const __nv_bfloat16 *__
           for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
 #pragma unroll
           for (int d = 8; d >= 1; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-          dyn_scale(amax, s, inv);
+          dyn_scale<kTimes>(amax, s, inv);
         } else {
           inv = inv_static;
         }
@@ -211,6 +218,57 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const __nv_bfloat16 *__
       }
     }
   }
+}
+
+template <bool kDynamic, bool kColMult>
+__global__ void __launch_bounds__(256) quant_rows_kernel(const __nv_bfloat16 *__restrict__ x, int64_t rows,
+                                                         int64_t cols, const float *__restrict__ static_scale,
+                                                         const float *__restrict__ col_scale,
+                                                         const int *__restrict__ offs, int G,
+                                                         uint8_t *__restrict__ codes, float *__restrict__ scales,
+                                                         uint32_t *__restrict__ status) {
+  quant_rows_of<kDynamic, kColMult>(blockIdx.x, gridDim.x, x, rows, cols, static_scale, col_scale, offs, G, codes,
+                                    scales, status);
+}
+
+// The group plan (block 0) and the row quantizer (the other blocks, which need
+// no plan) in one launch, for calls where launches count.  The plan resets the
+// status word, which may lose a bad static scale that the quantizer reports
+// first: the GEMM that follows reports it again.  The block scale is a product
+// with 1 / 448, which is what torch makes of a tensor divided by a constant: a
+// reference in torch then has the same codes.  (x / s of two bf16 values often
+// falls exactly between two codes, so that one ulp of s decides it: outputs
+// differed by 0.003 to 0.005 of their norm from such a reference.)
+template <bool kDynamic>
+__global__ void __launch_bounds__(256) plan_quant_rows_kernel(const int32_t *__restrict__ sizes, int G, int64_t M,
+                                                              int *__restrict__ offs, int *__restrict__ tpre,
+                                                              const __nv_bfloat16 *__restrict__ x, int64_t cols,
+                                                              const float *__restrict__ static_scale,
+                                                              uint8_t *__restrict__ codes, float *__restrict__ scales,
+                                                              uint32_t *__restrict__ status) {
+  if (blockIdx.x == 0) {
+    if (threadIdx.x < 32) plan_groups(sizes, G, M, offs, tpre, status);
+  } else {
+    quant_rows_of<kDynamic, false, true>(blockIdx.x - 1, gridDim.x - 1, x, M, cols, static_scale, nullptr, nullptr, G, codes,
+                                   scales, status);
+  }
+}
+
+cudaError_t launch_plan_quant_rows(const int32_t *sizes, int G, int64_t M, int *offs, int *tpre, const void *x,
+                                   int64_t cols, bool dynamic, const float *static_scale, uint8_t *codes,
+                                   float *scales, uint32_t *status, cudaStream_t st) {
+  int64_t blocks = (M + 7) / 8;
+  const int64_t cap = static_cast<int64_t>(num_sms()) * 8;
+  if (blocks > cap) blocks = cap;
+  const unsigned grid = static_cast<unsigned>(blocks + 1);
+  const __nv_bfloat16 *xb = static_cast<const __nv_bfloat16 *>(x);
+  if (dynamic)
+    plan_quant_rows_kernel<true><<<grid, 256, 0, st>>>(sizes, G, M, offs, tpre, xb, cols, static_scale, codes, scales,
+                                                       status);
+  else
+    plan_quant_rows_kernel<false><<<grid, 256, 0, st>>>(sizes, G, M, offs, tpre, xb, cols, static_scale, codes, scales,
+                                                        status);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_quant_rows(const void *x, int64_t rows, int64_t cols, bool dynamic, const float *static_scale,

@@ -39,6 +39,15 @@ def act64(z, act):
     return z
 
 
+def torch_quantize(x):
+    """The dynamic rule of gmm_fwd_act in torch: codes [M, K], scales [K/128, M]."""
+    b = x.float().view(x.shape[0], -1, 128)
+    s = b.abs().amax(2, keepdim=True) / 448.0  # torch: times fl32(1/448)
+    inv = torch.where(s > 0, 1.0 / s, torch.zeros_like(s))
+    q = (b * inv).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8).view(x.shape)
+    return q, s[:, :, 0].t().contiguous()
+
+
 def _product(lhs, w, sizes, rule, trans, s):
     """rhs operands on the GPU, z64 and A of the product (rows outside groups 0)."""
     M, K = lhs.shape
@@ -50,7 +59,7 @@ def _product(lhs, w, sizes, rule, trans, s):
         rhs, sc = gm.gmm_quantize_rhs(w, transpose_out=trans)
         c, _ = gm.gmm_quantize_rhs(w)
         wd = c.view(torch.float8_e4m3fn).double() * sc.double()[:, None, :]
-        q, bs = gm.gmm_quantize(lhs, rule, axis=1, static_scale=s if rule == "static" else None)
+        q, bs = torch_quantize(lhs) if rule == "dynamic" else (*gm.gmm_quantize(lhs, rule, axis=1, static_scale=s)[:1], s)
         a = q.view(torch.float8_e4m3fn).double()
         a = a * s.double() if rule == "static" else (a.view(M, K // 128, 128) * bs.t().double()[:, :, None]).view(M, K)
     z = torch.zeros(M, N, dtype=torch.float64, device=DEV)
@@ -171,6 +180,8 @@ def test_plain_epilogue_equals_gmm_fwd():
     codes, sc = gm.gmm_quantize_rhs(w)
     for rule in ("static", "dynamic"):
         kw = dict(rule=rule, static_scale=s if rule == "static" else None)
+        if rule == "dynamic":  # the same codes for both (the scales' one ulp aside)
+            lhs, kw["lhs_scales"] = gm.gmm_quantize(lhs, "dynamic", axis=1)
         assert torch.equal(gm.gmm_fwd_act(lhs, codes, sc, gs, **kw), gm.gmm_fwd(lhs, codes, sc, gs, **kw))
         a = gm.gmm_fwd_act(lhs, codes, sc, gs, act="swiglu", **kw).double()
         b = gm.gmm_fwd_swiglu(lhs, codes, sc, gs, **kw).double()
@@ -183,13 +194,16 @@ def test_block_scaled_weights_and_quantized_lhs():
     codes, bs = gm.gmm_quantize_rhs_blocks(w, axis=0)
     for rule in ("static", "dynamic"):
         kw = dict(rule=rule, static_scale=s if rule == "static" else None)
-        z, ab0 = gm.gmm_fwd(lhs, codes, bs, gs, out_dtype=torch.float32, **kw).double(), None
-        y = gm.gmm_fwd_act(lhs, codes, bs, gs, act="silu", bias=bias, out_dtype=torch.float32, **kw)
+        x = lhs
+        if rule == "dynamic":
+            x, kw["lhs_scales"] = gm.gmm_quantize(lhs, "dynamic", axis=1)
+        z, ab0 = gm.gmm_fwd(x, codes, bs, gs, out_dtype=torch.float32, **kw).double(), None
+        y = gm.gmm_fwd_act(x, codes, bs, gs, act="silu", bias=bias, out_dtype=torch.float32, **kw)
         ref = act64(z + _bias_rows(bias, sizes, M), "silu")
         ref[150:] = 0
         assert_within(y, ref.cpu().numpy(), (1e-5 * ref.abs() + 1e-6 * (z.abs() + 1)).cpu().numpy(), rule)
         assert ab0 is None
-    q, qs = gm.gmm_quantize(lhs, "dynamic", axis=1)
+    q, qs = torch_quantize(lhs)  # bit for bit what the call makes of lhs
     c2, s2 = gm.gmm_quantize_rhs(w)
     a = gm.gmm_fwd_act(q, c2, s2, gs, act="gelu", bias=bias, rule="dynamic", lhs_scales=qs)
     assert torch.equal(a, gm.gmm_fwd_act(lhs, c2, s2, gs, act="gelu", bias=bias, rule="dynamic"))
@@ -358,3 +372,19 @@ def test_streams_and_graphs():
     torch.cuda.synchronize()
     for o in outs:
         assert all(torch.equal(a, b) for a, b in zip(o, want))
+
+
+def test_device_errors():
+    lhs, w, bias, gs, s = _case([60, 200], 260, 256, 384, 8)
+    codes, sc = gm.gmm_quantize_rhs(w)
+    ws = torch.empty(gm.gmm_workspace_bytes(0, 260, 256, 384, 2), dtype=torch.uint8, device=DEV)
+    gm.gmm_fwd_act(lhs, codes, sc, gs, act="silu", bias=bias, static_scale=s, ws=ws)
+    assert gm.gmm_read_device_status(ws) == (0, 0)
+    out = gm.gmm_fwd_act(lhs, codes, sc, gs, act="silu", static_scale=torch.zeros_like(s), ws=ws)
+    assert gm.gmm_read_device_status(ws) == (4, 2) and bool((out == 0).all())  # an unusable scale
+    gm.gmm_fwd_act(lhs, codes, sc, torch.tensor([-1, 200], dtype=torch.int32, device=DEV), static_scale=s, ws=ws)
+    assert gm.gmm_read_device_status(ws)[0] == 7
+    z = torch.zeros(260, 384, dtype=torch.bfloat16, device=DEV)
+    ws2 = torch.empty(1 << 20, dtype=torch.uint8, device=DEV)
+    gm.gmm_act_bwd(z, z, torch.tensor([200, 200], dtype=torch.int32, device=DEV), act="gelu", ws=ws2)
+    assert gm.gmm_read_device_status(ws2)[0] == 7  # clamped to the rows there are
