@@ -3,12 +3,16 @@
 // activation and the residual.
 //
 // The E4M3 passes hold a thread's 128 accumulators in registers and finish them
-// 32 columns at a time, in one instantiation per activation (16 columns at a time, with narrower stores, ran 5 % slower; a
-// rolled loop over shifted accumulators 40 %: it spills them); the bf16 family
-// reads its chunks from TMEM in one rolled loop.  The activations' instructions
-// are what an epilogue is made of: with the exact library forms of act.cuh's
-// functions the Mixtral-like up projection took 2.4 ms with SiLU and 5.1 ms
-// with GELU, with these 1.62 and 1.70 ms (1.46 ms without an epilogue).
+// 32 columns at a time, in one instantiation per activation.  16 columns at a
+// time, with narrower stores, ran 5 % slower; a rolled loop over shifted
+// accumulators 40 % (it spills them); a chunk's residual loaded while the chunk
+// before it is finished 5 to 10 %.  The bf16 family reads its chunks from TMEM
+// in one rolled loop.  The activations' instructions are what an epilogue is
+// made of: with the exact library forms of act.cuh's functions the Mixtral-like
+// up projection took 2.4 ms with SiLU and 5.1 ms with GELU, with these 1.55 and
+// 1.57 ms (1.48 ms without an epilogue).  32 accumulator columns a TMEM load and
+// 232 registers a thread instead of 216 or 224 brought them there from 1.64 and
+// 1.66 ms, and SwiGLU with a bias and kept z from 1.71 to 1.58 ms.
 #pragma once
 
 #include <cuda_bf16.h>

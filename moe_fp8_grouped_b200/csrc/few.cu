@@ -395,7 +395,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   }
 
   const WaitCtl ctl{p.wait_limit_ns, &t.abort_flag, p.status};
-  const WaitCtl ctl_drain{p.wait_limit_ns, &t.no_abort, p.status};
+  // a CTA leaves only when its own copies and MMAs have landed, however short the caller's limit
+  const WaitCtl ctl_drain{max(p.wait_limit_ns, static_cast<uint64_t>(1000000000)), &t.no_abort, p.status};
   const Product prod1 = t.prod[0], prod2 = t.prod[1];
   const int n1 = prod1.n, n2 = prod2.n;
   // E4M3 weights use hi and lo columns, bf16 one column a row

@@ -43,11 +43,11 @@ constexpr int kNumBars = 48;      // mbarriers reserved in shared memory
 // two epilogue warpgroups.  Sum must not exceed the launch allocation
 // (registers per thread at launch x 384); launch_inst checks it.
 // The promote variants keep 128 accumulators per thread and get the larger
-// epilogue share.
-template <bool kPromote>
-constexpr int regs_ctl() { return kPromote ? 40 : 72; }
-template <bool kPromote>
-constexpr int regs_epi() { return kPromote ? 232 : 216; }
+// epilogue share, and so do the E4M3 products with a fused epilogue (kEpi >= 0).
+template <bool kPromote, int kEpi>
+constexpr int regs_ctl() { return kPromote || kEpi >= 0 ? 40 : 72; }
+template <bool kPromote, int kEpi>
+constexpr int regs_epi() { return kPromote || kEpi >= 0 ? 232 : 216; }
 
 // Pipeline stages.  One CTA: A 16 KB + B 32 KB per stage, 4 stages (tgmm: 3,
 // the freed shared memory stages its output for TMA stores, one 4 KB block
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const WaitCtl ctl_drain{p.wait_limit_ns, no_abort, p.status};
 
   if (warp < 4) {
-    setmaxnreg_dec<regs_ctl<kPromote>()>();
+    setmaxnreg_dec<regs_ctl<kPromote, kEpi>()>();
     if (warp == 0 && lane == 0) {
       // ---------------------------------------------------- TMA producer
       int it = 0;
@@ -550,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       cp_async_wait_all();  // no copy in flight when the warp leaves
     }
   } else {
-    setmaxnreg_inc<regs_epi<kPromote>()>();
+    setmaxnreg_inc<regs_epi<kPromote, kEpi>()>();
     // ---------------------------------------------------------- epilogue
     const int et = threadIdx.x - kEpiWarp0 * 32;  // 0 .. 255
     const int q = warp & 3, h = (warp - kEpiWarp0) >> 2;
@@ -781,17 +781,33 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.0f, 0.0f);
         for (int bi = 0; bi < (two ? 2 : 1); ++bi) {
+          if constexpr (kEpi != kNoEpi) {
+            // 32 columns a load: the fused epilogue leaves no registers for 64
 #pragma unroll
-          for (int cp = 0; cp < 2; ++cp) {
-            uint32_t va[32], vb[32];
-            tmem_ld64(tl + bi * kTN + colt(2 * cp), va, vb);
-            tmem_wait_ld();
+            for (int c = 0; c < 4; ++c) {
+              uint32_t va[32];
+              tmem_ld32(tl + bi * kTN + colt(c), va);
+              tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              acc[2 * cp * 16 + i] =
-                  __fadd2_rn(acc[2 * cp * 16 + i], make_float2(__uint_as_float(va[2 * i]), __uint_as_float(va[2 * i + 1])));
-              acc[(2 * cp + 1) * 16 + i] = __fadd2_rn(
-                  acc[(2 * cp + 1) * 16 + i], make_float2(__uint_as_float(vb[2 * i]), __uint_as_float(vb[2 * i + 1])));
+              for (int i = 0; i < 16; ++i)
+                acc[c * 16 + i] = __fadd2_rn(
+                    acc[c * 16 + i], make_float2(__uint_as_float(va[2 * i]), __uint_as_float(va[2 * i + 1])));
+            }
+          } else {
+#pragma unroll
+            for (int cp = 0; cp < 2; ++cp) {
+              uint32_t va[32], vb[32];
+              tmem_ld64(tl + bi * kTN + colt(2 * cp), va, vb);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                acc[2 * cp * 16 + i] =
+                    __fadd2_rn(acc[2 * cp * 16 + i],
+                               make_float2(__uint_as_float(va[2 * i]), __uint_as_float(va[2 * i + 1])));
+                acc[(2 * cp + 1) * 16 + i] = __fadd2_rn(
+                    acc[(2 * cp + 1) * 16 + i],
+                    make_float2(__uint_as_float(vb[2 * i]), __uint_as_float(vb[2 * i + 1])));
+              }
             }
           }
         }
@@ -951,7 +967,7 @@ static cudaError_t launch_inst(const CUtensorMap &tmA, const CUtensorMap &tmB, c
   if (e != cudaSuccess) return e;
   // setmaxnreg.inc waits for registers the CTA owns: never launch a split that
   // does not fit the launch allocation
-  if (attr.numRegs * kThreads < regs_ctl<kPromote>() * 128 + regs_epi<kPromote>() * 256)
+  if (attr.numRegs * kThreads < regs_ctl<kPromote, kEpi>() * 128 + regs_epi<kPromote, kEpi>() * 256)
     return cudaErrorInvalidConfiguration;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;

@@ -105,10 +105,15 @@ constexpr bool two_issuers() { return kPromote || (kElem == 1 && kMode != MODE_T
 // the larger epilogue share (the static row passes keep a little more for
 // their producer's SwiGLU box logic: fewer spills measured with 56 / 224 than
 // with 40 / 232).
-template <int kElem, bool kPromote, int kMode>
-constexpr int regs_ctl() { return kPromote ? 40 : (two_issuers<kElem, kPromote, kMode>() ? 56 : 72); }
-template <int kElem, bool kPromote, int kMode>
-constexpr int regs_epi() { return kPromote ? 232 : (two_issuers<kElem, kPromote, kMode>() ? 224 : 216); }
+// The E4M3 products with a fused epilogue (kEpi >= 0) take the larger share.
+template <int kElem, bool kPromote, int kMode, int kEpi>
+constexpr int regs_ctl() {
+  return kPromote || kEpi >= 0 ? 40 : (two_issuers<kElem, kPromote, kMode>() ? 56 : 72);
+}
+template <int kElem, bool kPromote, int kMode, int kEpi>
+constexpr int regs_epi() {
+  return kPromote || kEpi >= 0 ? 232 : (two_issuers<kElem, kPromote, kMode>() ? 224 : 216);
+}
 
 // tgmm keeps 3 pipeline stages and uses the freed shared memory to stage its
 // output for TMA stores (one 4 KB block per epilogue warp)
@@ -300,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const WaitCtl ctl_drain{p.wait_limit_ns, no_abort, p.status};
 
   if (warp < 4) {
-    setmaxnreg_dec<regs_ctl<kElem, kPromote, kMode>()>();
+    setmaxnreg_dec<regs_ctl<kElem, kPromote, kMode, kEpi>()>();
     if (warp == 0 && lane == 0) {
       // ---------------------------------------------------- TMA producer
       int it = 0;
@@ -494,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       cp_async_wait_all();  // no copy in flight when the warp leaves
     }
   } else {
-    setmaxnreg_inc<regs_epi<kElem, kPromote, kMode>()>();
+    setmaxnreg_inc<regs_epi<kElem, kPromote, kMode, kEpi>()>();
     // ---------------------------------------------------------- epilogue
     const int et = threadIdx.x - kEpiWarp0 * 32;  // 0 .. 255
     const int q = warp & 3, h = (warp - kEpiWarp0) >> 2;
@@ -731,18 +736,34 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.0f, 0.0f);
         for (int bi = 0; bi < (two ? 2 : 1); ++bi) {
+          if constexpr (kEpi != kNoEpi) {
+            // 32 columns a load: the fused epilogue leaves no registers for 64
 #pragma unroll
-          for (int cp = 0; cp < 2; ++cp) {
-            // chunks 2 cp, 2 cp + 1: colt(2 cp + 1) = colt(2 cp) + 32
-            uint32_t va[32], vb[32];
-            tmem_ld64(tl + bi * kBN + colt(2 * cp), va, vb);
-            tmem_wait_ld();
+            for (int c = 0; c < 4; ++c) {
+              uint32_t va[32];
+              tmem_ld32(tl + bi * kBN + colt(c), va);
+              tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              acc[2 * cp * 16 + i] =
-                  __fadd2_rn(acc[2 * cp * 16 + i], make_float2(__uint_as_float(va[2 * i]), __uint_as_float(va[2 * i + 1])));
-              acc[(2 * cp + 1) * 16 + i] = __fadd2_rn(
-                  acc[(2 * cp + 1) * 16 + i], make_float2(__uint_as_float(vb[2 * i]), __uint_as_float(vb[2 * i + 1])));
+              for (int i = 0; i < 16; ++i)
+                acc[c * 16 + i] = __fadd2_rn(
+                    acc[c * 16 + i], make_float2(__uint_as_float(va[2 * i]), __uint_as_float(va[2 * i + 1])));
+            }
+          } else {
+#pragma unroll
+            for (int cp = 0; cp < 2; ++cp) {
+              // chunks 2 cp, 2 cp + 1: colt(2 cp + 1) = colt(2 cp) + 32
+              uint32_t va[32], vb[32];
+              tmem_ld64(tl + bi * kBN + colt(2 * cp), va, vb);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                acc[2 * cp * 16 + i] =
+                    __fadd2_rn(acc[2 * cp * 16 + i],
+                               make_float2(__uint_as_float(va[2 * i]), __uint_as_float(va[2 * i + 1])));
+                acc[(2 * cp + 1) * 16 + i] = __fadd2_rn(
+                    acc[(2 * cp + 1) * 16 + i],
+                    make_float2(__uint_as_float(vb[2 * i]), __uint_as_float(vb[2 * i + 1])));
+              }
             }
           }
         }
@@ -903,7 +924,8 @@ static cudaError_t launch_inst(const CUtensorMap &tmA, const CUtensorMap &tmB, c
   if (e != cudaSuccess) return e;
   // setmaxnreg.inc waits for registers the CTA owns: never launch a split that
   // does not fit the launch allocation
-  if (attr.numRegs * kThreads < regs_ctl<kElem, kPromote, kMode>() * 128 + regs_epi<kElem, kPromote, kMode>() * 256)
+  if (attr.numRegs * kThreads <
+      regs_ctl<kElem, kPromote, kMode, kEpi>() * 128 + regs_epi<kElem, kPromote, kMode, kEpi>() * 256)
     return cudaErrorInvalidConfiguration;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
