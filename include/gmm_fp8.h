@@ -249,13 +249,14 @@ typedef struct {
  * With G = 1 this is a dense product.  A bf16 lhs with the dynamic rule gets
  * the block scales fl32(amax * fl32(1/448)), as torch divides a tensor by a
  * constant; gmm_fwd and gmm_quantize divide, at most one ulp away, so codes
- * that fall between two E4M3 values may differ.  All else of lhs, rhs, rules, layouts, group_sizes
- * and the workspace (gmm_workspace_bytes(GMM_OP_FWD, M, K, N, G)) are
- * gmm_fwd's; z, the activation and the sum are fp32, rounded once to out and
- * (on its own) to preact.  Nout = N, or N / 2 for GMM_ACT_SWIGLU, which takes
- * the merged gate|up weights of gmm_fwd_swiglu (N % 256 else GMM_ERR_SHAPE)
- * and a bias over all N columns.  Rows outside every group are 0 in out and
- * in preact.  The pages have no counterpart; the epilogue is this library's.
+ * that fall between two E4M3 values may differ.  All else of lhs, rhs, rules,
+ * layouts, group_sizes and the workspace (gmm_workspace_bytes(GMM_OP_FWD, M, K,
+ * N, G)) are gmm_fwd's; z, the activation and the sum are fp32, rounded once to
+ * out and (on its own) to preact.  Nout = N, or N / 2 for GMM_ACT_SWIGLU, which
+ * takes the merged gate|up weights of gmm_fwd_swiglu (N % 256 else
+ * GMM_ERR_SHAPE) and a bias over all N columns.  Rows outside every group are 0
+ * in out and in preact.  The pages have no counterpart; the epilogue is this
+ * library's.
  */
 gmm_status gmm_fwd_act(gmm_operand lhs, gmm_operand rhs, int transpose_rhs, const int32_t *group_sizes, int32_t G,
                        int64_t M, int64_t K, int64_t N, const gmm_epilogue *epi, void *out, gmm_dtype out_dtype,

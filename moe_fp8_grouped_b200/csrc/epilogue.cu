@@ -148,9 +148,11 @@ __global__ void __launch_bounds__(128) dbias_kernel(const float *__restrict__ pa
 }  // namespace
 
 cudaError_t launch_act_bwd(int act, const ActBwdParams &p, cudaStream_t st) {
-  // every tile of a group, then the slices of the rows behind the last group
+  // every tile of a group, then the slices of the rows behind the last group:
+  // n lengths of sum M have at most floor((M + 127 n) / 128) tiles of 128, which
+  // for n = G + 1 <= 1025 is at most ceil(M / 128) + G (and so below 2^16)
   const dim3 grid(static_cast<unsigned>((p.F + kActCols - 1) / kActCols),
-                  static_cast<unsigned>((p.M + kBlk - 1) / kBlk + p.G + 1));
+                  static_cast<unsigned>((p.M + kBlk - 1) / kBlk + p.G));
   switch (act) {
     case GMM_ACT_NONE: act_bwd_kernel<GMM_ACT_NONE><<<grid, kActThreads, 0, st>>>(p); break;
     case GMM_ACT_RELU: act_bwd_kernel<GMM_ACT_RELU><<<grid, kActThreads, 0, st>>>(p); break;

@@ -388,3 +388,16 @@ def test_device_errors():
     ws2 = torch.empty(1 << 20, dtype=torch.uint8, device=DEV)
     gm.gmm_act_bwd(z, z, torch.tensor([200, 200], dtype=torch.int32, device=DEV), act="gelu", ws=ws2)
     assert gm.gmm_read_device_status(ws2)[0] == 7  # clamped to the rows there are
+
+
+def test_bwd_at_the_most_rows():
+    """The largest row count that the library takes (ceil(M / 128) + G = 65535),
+    rows behind the last group among them."""
+    M, N, rows = 65534 * 128, 128, 8_000_001
+    z = torch.full((M, N), -1.0, dtype=torch.bfloat16, device=DEV)
+    z[::2] = 1.0
+    dout = torch.ones(M, N, dtype=torch.bfloat16, device=DEV)
+    gs = torch.tensor([rows], dtype=torch.int32, device=DEV)
+    dz, db = gm.gmm_act_bwd(dout, z, gs, act="relu")
+    assert bool((dz[0:rows:2] == 1).all()) and bool((dz[1:rows:2] == 0).all()) and bool((dz[rows:] == 0).all())
+    assert bool((db == 4_000_001).all())  # sums of ones below 2^24 are exact
