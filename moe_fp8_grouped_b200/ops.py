@@ -382,11 +382,45 @@ def _shape(t: torch.Tensor | None, name: str, shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
-def _scratch(ws: torch.Tensor | None, nbytes: int, like: torch.Tensor) -> torch.Tensor:
-    """The caller's workspace, or one from torch's caching allocator for this
-    call alone: the allocator keeps it apart per stream and per captured
-    graph, so that calls on several streams or in several graphs share none."""
-    return ws if ws is not None else like.new_empty(max(nbytes, 256), dtype=torch.uint8)
+_BF16, _F32, _I32 = (torch.bfloat16,), (torch.float32,), (torch.int32,)
+_FLOAT = (torch.bfloat16, torch.float32)
+_OPERAND = (torch.bfloat16, torch.uint8, torch.float8_e4m3fn)
+_U8 = (torch.uint8,)
+
+
+def _pointers(*args):
+    """Device pointers of a call's tensors.  Each argument: (tensor or None,
+    name, shape or None for any, dtypes).  All must be contiguous and on the
+    first tensor's CUDA device; _refuse words what is not so.  (One pass of
+    attribute reads: a check a function cost the smallest calls 4 us.)"""
+    dev = args[0][0].get_device()  # -1 for the CPU
+    ptrs = []
+    for t, name, shape, dtypes in args:
+        if t is None:
+            ptrs.append(None)
+            continue
+        if dev < 0 or t.get_device() != dev or t.dtype not in dtypes or not t.is_contiguous() or \
+                (shape is not None and t.shape != shape):
+            _refuse(args)
+        ptrs.append(t.data_ptr())
+    return ptrs
+
+
+def _refuse(args):
+    for t, name, shape, _ in args:
+        if shape is not None:
+            _shape(t, name, shape)
+    _same_device(*(a[0] for a in args))
+    for t, name, _, dtypes in args:
+        _dev(t, name, dtypes)
+    raise ValueError("unusable tensors")
+
+
+def _scratch(nbytes: int, like: torch.Tensor) -> torch.Tensor:
+    """A workspace from torch's caching allocator for one call alone: the
+    allocator keeps it apart per stream and per captured graph, so that calls
+    on several streams or in several graphs share none."""
+    return like.new_empty(max(nbytes, 256), dtype=torch.uint8)
 
 
 def gmm_fwd_act(lhs: torch.Tensor, rhs: torch.Tensor, rhs_scales: torch.Tensor | None, group_sizes: torch.Tensor,
@@ -409,32 +443,32 @@ def gmm_fwd_act(lhs: torch.Tensor, rhs: torch.Tensor, rhs_scales: torch.Tensor |
         raise ValueError(f"lhs contracts over {K}, rhs over {K2}")
     r = _rule(rule)
     out_shape = (M, N // 2 if act == "swiglu" else N)
-    _shape(bias, "bias", (G, N))
-    _shape(residual, "residual", out_shape)
-    _shape(out, "out", out_shape)
-    _shape(preact, "preact", (M, N))
-    _shape(group_sizes, "group_sizes", (G,))
-    _same_device(lhs, rhs, rhs_scales, group_sizes, bias, residual, out, ws, preact, static_scale, lhs_scales)
-    if lhs.dtype in (torch.uint8, torch.float8_e4m3fn):
-        sc = static_scale if r == B.Q_STATIC else lhs_scales
-        a = _operand(_dev(lhs, "lhs"), B.DT_E4M3, _dev(sc, "lhs scale", torch.float32), r)
-    else:
-        a = _operand(_dev(lhs, "lhs", torch.bfloat16), B.DT_BF16, _dev(static_scale, "static_scale", torch.float32), r)
-    if preact is None and keep_preact:
-        preact = lhs.new_empty((M, N), dtype=torch.bfloat16)
     if out is None:
         out = lhs.new_empty(out_shape, dtype=out_dtype)
-    epi = B.Epilogue(a_code, _dev(bias, "bias", torch.float32),
-                     _dev(residual, "residual", (torch.bfloat16, torch.float32)),
-                     _TORCH_DT[residual.dtype] if residual is not None else B.DT_BF16,
-                     _dev(preact, "preact", torch.bfloat16))
+    if preact is None and keep_preact:
+        preact = lhs.new_empty((M, N), dtype=torch.bfloat16)
+    if ws is None:
+        ws = _scratch(_fwd_bytes(M, K, N, G), lhs)
+    blockwise = rhs_scales is not None and rhs_scales.dim() == 3
+    if lhs.dtype == torch.bfloat16:
+        lhs_dt, sc, sc_shape = B.DT_BF16, static_scale, None
+    else:
+        lhs_dt, sc = B.DT_E4M3, static_scale if r == B.Q_STATIC else lhs_scales
+        sc_shape = None if r == B.Q_STATIC else (K // 128, M)
+    a_p, w_p, ws_p, gs_p, out_p, sc_p, wsc_p, bias_p, res_p, z_p = _pointers(
+        (lhs, "lhs", None, _OPERAND), (rhs, "rhs", None, _OPERAND), (ws, "ws", None, _U8),
+        (group_sizes, "group_sizes", (G,), _I32), (out, "out", out_shape, _FLOAT),
+        (sc, "lhs scale", sc_shape, _F32),
+        (rhs_scales, "rhs_scales", (G, K // 128, N) if blockwise else (G, N), _F32), (bias, "bias", (G, N), _F32),
+        (residual, "residual", out_shape, _FLOAT), (preact, "preact", (M, N), _BF16))
+    epi = B.Epilogue(a_code, bias_p, res_p, _TORCH_DT[residual.dtype] if res_p is not None else B.DT_BF16, z_p)
     with _on(lhs):
-        ws = _scratch(ws, _fwd_bytes(M, K, N, G), lhs)
-        st = B.lib().gmm_fwd_act(a, _rhs_operand(rhs, rhs_scales), int(transpose_rhs),
-                                 _dev(group_sizes, "group_sizes", torch.int32), G, M, K, N, ctypes.byref(epi),
-                                 _dev(out, "out", (torch.bfloat16, torch.float32)), _TORCH_DT[out.dtype],
-                                 _dev(ws, "ws"), ws.numel(), _current(lhs))
-    _check(st, "gmm_fwd_act")
+        st = B.lib().gmm_fwd_act(B.Operand(a_p, lhs_dt, sc_p, r),
+                                 B.Operand(w_p, _TORCH_DT[rhs.dtype], wsc_p, B.Q_DYNAMIC if blockwise else B.Q_NONE),
+                                 int(transpose_rhs), gs_p, G, M, K, N, ctypes.byref(epi), out_p,
+                                 _TORCH_DT[out.dtype], ws_p, ws.numel(), _current(lhs))
+    if st != B.GMM_OK:
+        raise GmmError(st, "gmm_fwd_act")
     return out if preact is None else (out, preact)
 
 
@@ -447,21 +481,20 @@ def gmm_act_bwd(dout: torch.Tensor, preact: torch.Tensor, group_sizes: torch.Ten
     a_code = _name(ACTS, act, "act")
     M, N = preact.shape
     G = int(group_sizes.numel())
-    _shape(dout, "dout", (M, N // 2 if act == "swiglu" else N))
-    _shape(dz, "dz", (M, N))
-    _shape(dbias, "dbias", (G, N))
-    _same_device(dout, preact, group_sizes, dz, dbias, ws)
     if dz is None:
         dz = dout.new_empty((M, N), dtype=torch.bfloat16)
     if dbias is None and with_dbias:
         dbias = dout.new_empty((G, N), dtype=torch.float32)
+    if ws is None:
+        ws = _scratch(_act_bwd_bytes(M, N, G), dout)
+    dout_p, z_p, gs_p, dz_p, db_p, ws_p = _pointers(
+        (dout, "dout", (M, N // 2 if act == "swiglu" else N), _BF16), (preact, "preact", None, _BF16),
+        (group_sizes, "group_sizes", None, _I32), (dz, "dz", (M, N), _BF16), (dbias, "dbias", (G, N), _F32),
+        (ws, "ws", None, _U8))
     with _on(dout):
-        ws = _scratch(ws, _act_bwd_bytes(M, N, G), dout)
-        st = B.lib().gmm_act_bwd(_dev(dout, "dout", torch.bfloat16), _dev(preact, "preact", torch.bfloat16), a_code,
-                                 _dev(group_sizes, "group_sizes", torch.int32), G, M, N,
-                                 _dev(dz, "dz", torch.bfloat16), _dev(dbias, "dbias", torch.float32), _dev(ws, "ws"),
-                                 ws.numel(), _current(dout))
-    _check(st, "gmm_act_bwd")
+        st = B.lib().gmm_act_bwd(dout_p, z_p, a_code, gs_p, G, M, N, dz_p, db_p, ws_p, ws.numel(), _current(dout))
+    if st != B.GMM_OK:
+        raise GmmError(st, "gmm_act_bwd")
     return dz, dbias
 
 
@@ -482,27 +515,21 @@ def gmm_moe_few(x: torch.Tensor, expert_ids: torch.Tensor, weights: torch.Tensor
     G2, F, N = (w2.shape[0], w2.shape[2], w2.shape[1]) if transpose_rhs else w2.shape
     if K2 != K or G2 != G or F2 != 2 * F:
         raise ValueError(f"x {tuple(x.shape)}, w1 {tuple(w1.shape)} and w2 {tuple(w2.shape)} do not fit together")
-    _shape(expert_ids, "expert_ids", (T, k))
-    _shape(weights, "weights", (T, k))
-    _shape(w1_scales, "w1_scales", (G, F2))
-    _shape(w2_scales, "w2_scales", (G, N))
-    _shape(out, "out", (T, N))
-    _same_device(x, expert_ids, weights, w1, w1_scales, w2, w2_scales, out, ws)
-    if w1.dtype not in _TORCH_DT or w2.dtype not in _TORCH_DT:
-        raise ValueError(f"w1 / w2 have dtype {w1.dtype} / {w2.dtype}, expected E4M3 codes or bf16")
-    dt = _TORCH_DT[w1.dtype]
     if out is None:
         out = x.new_empty((T, N), dtype=out_dtype)
+    dt = _TORCH_DT.get(w1.dtype, B.DT_F32)
+    if ws is None:
+        ws = _scratch(_few_bytes(T, k, G, K, F, N, dt), x)
+    x_p, ids_p, wt_p, w1_p, s1_p, w2_p, s2_p, y_p, ws_p = _pointers(
+        (x, "x", None, _BF16), (expert_ids, "expert_ids", (T, k), _I32), (weights, "weights", (T, k), _F32),
+        (w1, "w1", None, _OPERAND), (w1_scales, "w1_scales", (G, F2), _F32), (w2, "w2", None, _OPERAND),
+        (w2_scales, "w2_scales", (G, N), _F32), (out, "out", (T, N), _FLOAT), (ws, "ws", None, _U8))
     with _on(x):
-        ws = _scratch(ws, _few_bytes(T, k, G, K, F, N, dt), x)
-        st = B.lib().gmm_moe_few(
-            _dev(x, "x", torch.bfloat16), _dev(expert_ids, "expert_ids", torch.int32),
-            _dev(weights, "weights", torch.float32), T, k,
-            _operand(_dev(w1, "w1"), dt, _dev(w1_scales, "w1_scales", torch.float32), B.Q_NONE),
-            _operand(_dev(w2, "w2"), _TORCH_DT[w2.dtype], _dev(w2_scales, "w2_scales", torch.float32), B.Q_NONE),
-            int(transpose_rhs), G, K, F, N, _dev(out, "out", (torch.bfloat16, torch.float32)), _TORCH_DT[out.dtype],
-            _dev(ws, "ws"), ws.numel(), _current(x))
-    _check(st, "gmm_moe_few")
+        st = B.lib().gmm_moe_few(x_p, ids_p, wt_p, T, k, B.Operand(w1_p, dt, s1_p, B.Q_NONE),
+                                 B.Operand(w2_p, _TORCH_DT[w2.dtype], s2_p, B.Q_NONE), int(transpose_rhs), G, K, F, N,
+                                 y_p, _TORCH_DT[out.dtype], ws_p, ws.numel(), _current(x))
+    if st != B.GMM_OK:
+        raise GmmError(st, "gmm_moe_few")
     return out
 
 
@@ -514,16 +541,15 @@ def gmm_router_topk(logits: torch.Tensor, k: int, score: str = "softmax", select
     scale * score / (sum of the chosen scores).  Experts masked with -inf are
     never chosen (id -1, weight 0 where fewer than k are left)."""
     T, E = logits.shape
-    _shape(select_bias, "select_bias", (E,))
-    _same_device(logits, select_bias)
     ids = logits.new_empty((T, k), dtype=torch.int32)
     weights = logits.new_empty((T, k), dtype=torch.float32)
+    x_p, bias_p = _pointers((logits, "logits", None, _FLOAT), (select_bias, "select_bias", (E,), _F32))
     with _on(logits):
-        st = B.lib().gmm_router_topk(_dev(logits, "logits", (torch.float32, torch.bfloat16)), _TORCH_DT[logits.dtype],
-                                     T, E, k, _name(SCORES, score, "score"),
-                                     _dev(select_bias, "select_bias", torch.float32), int(normalize), float(scale),
-                                     ids.data_ptr(), weights.data_ptr(), _current(logits))
-    _check(st, "gmm_router_topk")
+        st = B.lib().gmm_router_topk(x_p, _TORCH_DT[logits.dtype], T, E, k, _name(SCORES, score, "score"), bias_p,
+                                     int(normalize), float(scale), ids.data_ptr(), weights.data_ptr(),
+                                     _current(logits))
+    if st != B.GMM_OK:
+        raise GmmError(st, "gmm_router_topk")
     return ids, weights
 
 
@@ -533,17 +559,15 @@ def gmm_router_topk_bwd(dweights: torch.Tensor, logits: torch.Tensor, expert_ids
     from dweights [T, k] fp32, the logits and the chosen expert_ids."""
     T, E = logits.shape
     k = expert_ids.shape[1]
-    _shape(expert_ids, "expert_ids", (T, k))
-    _shape(dweights, "dweights", (T, k))
-    _same_device(logits, dweights, expert_ids)
     dlogits = torch.empty_like(logits)
+    x_p, dw_p, ids_p = _pointers((logits, "logits", None, _FLOAT), (dweights, "dweights", (T, k), _F32),
+                                 (expert_ids, "expert_ids", (T, k), _I32))
     with _on(logits):
-        st = B.lib().gmm_router_topk_bwd(_dev(dweights, "dweights", torch.float32),
-                                         _dev(logits, "logits", (torch.float32, torch.bfloat16)),
-                                         _TORCH_DT[logits.dtype], _dev(expert_ids, "expert_ids", torch.int32), T, E, k,
+        st = B.lib().gmm_router_topk_bwd(dw_p, x_p, _TORCH_DT[logits.dtype], ids_p, T, E, k,
                                          _name(SCORES, score, "score"), int(normalize), float(scale),
                                          dlogits.data_ptr(), _current(logits))
-    _check(st, "gmm_router_topk_bwd")
+    if st != B.GMM_OK:
+        raise GmmError(st, "gmm_router_topk_bwd")
     return dlogits
 
 
@@ -552,14 +576,14 @@ def gmm_combine_dweight(dy: torch.Tensor, rows: torch.Tensor, slot: torch.Tensor
     sum_n dy[t, n] * rows[slot[t, j], n] (fp32 [T, k]; 0 for a slot outside
     rows).  dy [T, N] and rows [R, N] bf16, slot int32 [T, k]."""
     T, k = slot.shape
-    _shape(dy, "dy", (T, rows.shape[1]))
-    _same_device(dy, rows, slot)
+    R, N = rows.shape
     dw = dy.new_empty((T, k), dtype=torch.float32)
+    dy_p, rows_p, slot_p = _pointers((dy, "dy", (T, N), _BF16), (rows, "rows", None, _BF16),
+                                     (slot, "slot", None, _I32))
     with _on(dy):
-        st = B.lib().gmm_combine_dweight(_dev(dy, "dy", torch.bfloat16), _dev(rows, "rows", torch.bfloat16),
-                                         rows.shape[0], _dev(slot, "slot", torch.int32), T, k, rows.shape[1],
-                                         dw.data_ptr(), _current(dy))
-    _check(st, "gmm_combine_dweight")
+        st = B.lib().gmm_combine_dweight(dy_p, rows_p, R, slot_p, T, k, N, dw.data_ptr(), _current(dy))
+    if st != B.GMM_OK:
+        raise GmmError(st, "gmm_combine_dweight")
     return dw
 
 

@@ -401,3 +401,44 @@ def test_bwd_at_the_most_rows():
     dz, db = gm.gmm_act_bwd(dout, z, gs, act="relu")
     assert bool((dz[0:rows:2] == 1).all()) and bool((dz[1:rows:2] == 0).all()) and bool((dz[rows:] == 0).all())
     assert bool((db == 4_000_001).all())  # sums of ones below 2^24 are exact
+
+
+def test_bwd_many_tiles_in_a_graph():
+    """Groups of many tiles, summed by whichever CTA ends last: the same bits
+    from every call and every replay, and the empty groups' zeros each time."""
+    sizes, M, N = [0, 5000, 0, 0, 129, 128, 0], 5300, 512
+    g = torch.Generator().manual_seed(9)
+    z = torch.randn(M, N, generator=g).bfloat16().to(DEV)
+    dout = torch.randn(M, N, generator=g).bfloat16().to(DEV)
+    gs = torch.tensor(sizes, dtype=torch.int32, device=DEV)
+    dz, db = gm.gmm_act_bwd(dout, z, gs, act="silu")
+    _, mag, rb, bm = _bwd_ref(z, dout, sizes, "silu")
+    # chains of 16 rows, 8 row threads, 5 tiles of each of 8 sums, those 8
+    assert_within(db, rb.cpu().numpy(), ((2e-6 + 40 * 2.0 ** -24) * bm + 1e-30).cpu().numpy(), "dbias")
+    out = torch.empty_like(db)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gm.gmm_act_bwd(dout, z, gs, act="silu", dbias=out)
+    for _ in range(5):
+        out.fill_(7.0)
+        graph.replay()
+        assert torch.equal(out, db)
+
+
+def test_wrong_scales_are_refused():
+    """Scales of another shape than the codes' would be read out of bounds."""
+    lhs, w, bias, gs, s = _case([60, 200], 260, 256, 384, 8)
+    codes, sc = gm.gmm_quantize_rhs(w)
+    with pytest.raises(ValueError, match="rhs_scales has shape"):
+        gm.gmm_fwd_act(lhs, codes, sc[:1], gs, static_scale=s)
+    with pytest.raises(ValueError, match="rhs_scales has shape"):
+        gm.gmm_fwd_act(lhs, codes, sc[None], gs, static_scale=s)
+    a, a_sc = gm.gmm_quantize(lhs, rule="dynamic", axis=1)
+    with pytest.raises(ValueError, match="lhs scale has shape"):
+        gm.gmm_fwd_act(a, codes, sc, gs, rule="dynamic", lhs_scales=a_sc[:, :100].contiguous())
+    with pytest.raises(ValueError, match="bias has dtype"):
+        gm.gmm_fwd_act(lhs, codes, sc, gs, bias=bias.bfloat16(), static_scale=s)
+    with pytest.raises(ValueError, match="must be contiguous"):
+        gm.gmm_fwd_act(lhs.t().contiguous().t(), codes, sc, gs, static_scale=s)
+    with pytest.raises(ValueError, match="all must be on one device"):
+        gm.gmm_fwd_act(lhs, codes, sc, gs.cpu(), static_scale=s)
