@@ -748,16 +748,18 @@ gmm_status gmm_backward(gmm_operand lhs, gmm_operand dout, gmm_operand rhs, int 
 
 static bool is_act(int a) { return a >= GMM_ACT_NONE && a <= GMM_ACT_SWIGLU; }
 
-// Workspace of gmm_act_bwd: status header, group plan, column sums per tile.
+// Workspace of gmm_act_bwd: status header, group plan, and for the bias
+// gradient the tiles' counters and column sums.
 struct ActBwdLayout {
-  size_t offs, tpre, partial, total;
+  size_t offs, tpre, done, partial, total;
 };
 
 static ActBwdLayout act_bwd_layout(int64_t M, int64_t N, int32_t G) {
   ActBwdLayout L;
   L.offs = sizeof(WsHeader);
   L.tpre = L.offs + align256(sizeof(int) * (G + 1));
-  L.partial = L.tpre + align256(sizeof(int) * (G + 1));
+  L.done = L.tpre + align256(sizeof(int) * (G + 1));
+  L.partial = L.done + align256(sizeof(uint32_t) * static_cast<size_t>(act_bwd_counters(N, G)));
   L.total = L.partial + align256(sizeof(float) * static_cast<size_t>(chunk_capacity(M, G)) * N);
   return L;
 }
@@ -823,13 +825,15 @@ gmm_status gmm_act_bwd(const void *dout_bf16, const void *preact_bf16, gmm_act a
   if (!al16(dout_bf16) || !al16(preact_bf16) || !al16(dz_bf16) || !al16(ws) || (dbias && !al16(dbias)))
     return GMM_ERR_ALIGNMENT;
   const ActBwdLayout L = act_bwd_layout(M, N, G);
-  if (!ws || ws_bytes < (dbias ? L.total : L.partial)) return GMM_ERR_WORKSPACE;
+  if (!ws || ws_bytes < (dbias ? L.total : L.done)) return GMM_ERR_WORKSPACE;
   uint8_t *w = static_cast<uint8_t *>(ws);
   ActBwdParams p{};
   p.dout = static_cast<const __nv_bfloat16 *>(dout_bf16);
   p.z = static_cast<const __nv_bfloat16 *>(preact_bf16);
   p.dz = static_cast<__nv_bfloat16 *>(dz_bf16);
-  p.partial = dbias ? reinterpret_cast<float *>(w + L.partial) : nullptr;
+  p.partial = reinterpret_cast<float *>(w + L.partial);
+  p.done = reinterpret_cast<uint32_t *>(w + L.done);
+  p.dbias = dbias;
   int *offs = reinterpret_cast<int *>(w + L.offs), *tpre = reinterpret_cast<int *>(w + L.tpre);
   p.offs = offs;
   p.tpre = tpre;
@@ -838,14 +842,13 @@ gmm_status gmm_act_bwd(const void *dout_bf16, const void *preact_bf16, gmm_act a
   p.N = N;
   p.F = act == GMM_ACT_SWIGLU ? N / 2 : N;
   s = cuda_status(prof("plan", st, [&] {
-    return launch_plan(group_sizes, G, M, offs, tpre, reinterpret_cast<uint32_t *>(w), st);
+    uint32_t *status = reinterpret_cast<uint32_t *>(w);
+    return dbias ? launch_plan_zero(group_sizes, G, M, offs, tpre, status, p.done, act_bwd_counters(N, G), st)
+                 : launch_plan(group_sizes, G, M, offs, tpre, status, st);
   }));
   if (s != GMM_OK) return s;
   if ((s = cuda_status(prof("act_bwd", st, [&] { return launch_act_bwd(act, p, st); }))) != GMM_OK) return s;
-  if (dbias &&
-      (s = cuda_status(prof("dbias", st, [&] { return launch_dbias(p.partial, tpre, G, N, dbias, st); }))) != GMM_OK)
-    return s;
-  g_launches = dbias ? 3 : 2;
+  g_launches = 2;
   return GMM_OK;
 }
 

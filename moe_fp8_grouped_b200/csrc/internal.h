@@ -42,6 +42,10 @@ WsLayout ws_layout(gmm_op op, int64_t M, int64_t K, int64_t N, int32_t G);
 cudaError_t launch_plan(const int32_t *sizes, int G, int64_t M, int *offs, int *tpre, uint32_t *status,
                         cudaStream_t st);
 
+// launch_plan and n counters set to 0, in one launch.
+cudaError_t launch_plan_zero(const int32_t *sizes, int G, int64_t M, int *offs, int *tpre, uint32_t *status,
+                             uint32_t *counters, int64_t n, cudaStream_t st);
+
 // Row quantizer (axis 1).  static_scale != NULL selects the static rule;
 // col_scale != NULL folds col_scale[g(m), n] in (needs offs).
 cudaError_t launch_quant_rows(const void *x, int64_t rows, int64_t cols, bool dynamic, const float *static_scale,

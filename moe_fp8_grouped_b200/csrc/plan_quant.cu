@@ -75,6 +75,27 @@ __global__ void plan_kernel(const int32_t *__restrict__ sizes, int G, int64_t M,
   plan_groups(sizes, G, M, offs, tpre, status);
 }
 
+// The plan (block 0) and n zeroed counters (the other blocks).
+__global__ void __launch_bounds__(256) plan_zero_kernel(const int32_t *__restrict__ sizes, int G, int64_t M,
+                                                        int *__restrict__ offs, int *__restrict__ tpre,
+                                                        uint32_t *__restrict__ status, uint32_t *__restrict__ counters,
+                                                        int64_t n) {
+  cudaTriggerProgrammaticLaunchCompletion();  // act_bwd may start and wait for this kernel's end
+  if (blockIdx.x == 0) {
+    if (threadIdx.x < 32) plan_groups(sizes, G, M, offs, tpre, status);
+  } else {
+    const int64_t i = static_cast<int64_t>(blockIdx.x - 1) * 256 + threadIdx.x;
+    if (i < n) counters[i] = 0;
+  }
+}
+
+cudaError_t launch_plan_zero(const int32_t *sizes, int G, int64_t M, int *offs, int *tpre, uint32_t *status,
+                             uint32_t *counters, int64_t n, cudaStream_t st) {
+  plan_zero_kernel<<<static_cast<unsigned>(1 + (n + 255) / 256), 256, 0, st>>>(sizes, G, M, offs, tpre, status,
+                                                                              counters, n);
+  return cudaGetLastError();
+}
+
 cudaError_t launch_plan(const int32_t *sizes, int G, int64_t M, int *offs, int *tpre, uint32_t *status,
                         cudaStream_t st) {
   plan_kernel<<<1, 32, 0, st>>>(sizes, G, M, offs, tpre, status);
