@@ -382,6 +382,11 @@ def _shape(t: torch.Tensor | None, name: str, shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
+def _empty(like: torch.Tensor, shape, dtype) -> torch.Tensor:
+    """like.new_empty for two dimensions, in 1.4 us of the host instead of 2."""
+    return torch.empty_strided(shape, (shape[1], 1), dtype=dtype, device=like.device)
+
+
 _BF16, _F32, _I32 = (torch.bfloat16,), (torch.float32,), (torch.int32,)
 _FLOAT = (torch.bfloat16, torch.float32)
 _OPERAND = (torch.bfloat16, torch.uint8, torch.float8_e4m3fn)
@@ -444,9 +449,9 @@ def gmm_fwd_act(lhs: torch.Tensor, rhs: torch.Tensor, rhs_scales: torch.Tensor |
     r = _rule(rule)
     out_shape = (M, N // 2 if act == "swiglu" else N)
     if out is None:
-        out = lhs.new_empty(out_shape, dtype=out_dtype)
+        out = _empty(lhs, out_shape, out_dtype)
     if preact is None and keep_preact:
-        preact = lhs.new_empty((M, N), dtype=torch.bfloat16)
+        preact = _empty(lhs, (M, N), torch.bfloat16)
     if ws is None:
         ws = _scratch(_fwd_bytes(M, K, N, G), lhs)
     blockwise = rhs_scales is not None and rhs_scales.dim() == 3
@@ -482,9 +487,9 @@ def gmm_act_bwd(dout: torch.Tensor, preact: torch.Tensor, group_sizes: torch.Ten
     M, N = preact.shape
     G = int(group_sizes.numel())
     if dz is None:
-        dz = dout.new_empty((M, N), dtype=torch.bfloat16)
+        dz = _empty(dout, (M, N), torch.bfloat16)
     if dbias is None and with_dbias:
-        dbias = dout.new_empty((G, N), dtype=torch.float32)
+        dbias = _empty(dout, (G, N), torch.float32)
     if ws is None:
         ws = _scratch(_act_bwd_bytes(M, N, G), dout)
     dout_p, z_p, gs_p, dz_p, db_p, ws_p = _pointers(
@@ -516,7 +521,7 @@ def gmm_moe_few(x: torch.Tensor, expert_ids: torch.Tensor, weights: torch.Tensor
     if K2 != K or G2 != G or F2 != 2 * F:
         raise ValueError(f"x {tuple(x.shape)}, w1 {tuple(w1.shape)} and w2 {tuple(w2.shape)} do not fit together")
     if out is None:
-        out = x.new_empty((T, N), dtype=out_dtype)
+        out = _empty(x, (T, N), out_dtype)
     dt = _TORCH_DT.get(w1.dtype, B.DT_F32)
     if ws is None:
         ws = _scratch(_few_bytes(T, k, G, K, F, N, dt), x)
@@ -541,8 +546,8 @@ def gmm_router_topk(logits: torch.Tensor, k: int, score: str = "softmax", select
     scale * score / (sum of the chosen scores).  Experts masked with -inf are
     never chosen (id -1, weight 0 where fewer than k are left)."""
     T, E = logits.shape
-    ids = logits.new_empty((T, k), dtype=torch.int32)
-    weights = logits.new_empty((T, k), dtype=torch.float32)
+    ids = _empty(logits, (T, k), torch.int32)
+    weights = _empty(logits, (T, k), torch.float32)
     x_p, bias_p = _pointers((logits, "logits", None, _FLOAT), (select_bias, "select_bias", (E,), _F32))
     with _on(logits):
         st = B.lib().gmm_router_topk(x_p, _TORCH_DT[logits.dtype], T, E, k, _name(SCORES, score, "score"), bias_p,
@@ -577,7 +582,7 @@ def gmm_combine_dweight(dy: torch.Tensor, rows: torch.Tensor, slot: torch.Tensor
     rows).  dy [T, N] and rows [R, N] bf16, slot int32 [T, k]."""
     T, k = slot.shape
     R, N = rows.shape
-    dw = dy.new_empty((T, k), dtype=torch.float32)
+    dw = _empty(dy, (T, k), torch.float32)
     dy_p, rows_p, slot_p = _pointers((dy, "dy", (T, N), _BF16), (rows, "rows", None, _BF16),
                                      (slot, "slot", None, _I32))
     with _on(dy):
