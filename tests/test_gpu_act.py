@@ -442,3 +442,29 @@ def test_wrong_scales_are_refused():
         gm.gmm_fwd_act(lhs.t().contiguous().t(), codes, sc, gs, static_scale=s)
     with pytest.raises(ValueError, match="all must be on one device"):
         gm.gmm_fwd_act(lhs, codes, sc, gs.cpu(), static_scale=s)
+
+
+@pytest.mark.parametrize("rule", ["static", "dynamic", "none"])
+def test_offsets_beyond_31_bits(rule):
+    """More than 2^31 values in out, z, residual and their gradients: the rows
+    at the end have the bits of a call with those rows alone."""
+    M, K, N, sizes = 1 << 18, 128, 8448, [100_000, 0, 160_000]
+    g = torch.Generator(device=DEV).manual_seed(4)
+    lhs = torch.randn(M, K, generator=g, device=DEV).bfloat16()
+    w = (torch.randn(3, K, N, generator=g, device=DEV) * 0.1).bfloat16()
+    bias = torch.randn(3, N, generator=g, device=DEV)
+    res = torch.empty(M, N, dtype=torch.bfloat16, device=DEV).normal_(generator=g)
+    rhs, sc = (w, None) if rule == "none" else gm.gmm_quantize_rhs(w)
+    s = torch.tensor([4.0 / 448.0], device=DEV) if rule == "static" else None
+    gs = torch.tensor(sizes, dtype=torch.int32, device=DEV)
+    out, z = gm.gmm_fwd_act(lhs, rhs, sc, gs, act="gelu", bias=bias, residual=res, rule=rule, static_scale=s,
+                            keep_preact=True)
+    dz, _ = gm.gmm_act_bwd(res, z, gs, act="gelu")
+    for grp, a, b in ((0, 0, 300), (2, 259_700, 260_000)):
+        one = torch.tensor([b - a], dtype=torch.int32, device=DEV)
+        o2, z2 = gm.gmm_fwd_act(lhs[a:b], rhs[grp:grp + 1], sc[grp:grp + 1] if sc is not None else None, one,
+                                act="gelu", bias=bias[grp:grp + 1], residual=res[a:b], rule=rule, static_scale=s,
+                                keep_preact=True)
+        assert torch.equal(out[a:b], o2) and torch.equal(z[a:b], z2)
+        assert torch.equal(dz[a:b], gm.gmm_act_bwd(res[a:b], z2, one, act="gelu", with_dbias=False)[0])
+    assert not bool(out[260_000:].any()) and not bool(z[260_000:].any()) and not bool(dz[260_000:].any())

@@ -305,3 +305,50 @@ def test_results_do_not_depend_on_the_other_tokens():
     pad_ids = torch.cat([ids, torch.full((2, k), -1, dtype=torch.int32, device=DEV)])
     padded = gm.gmm_moe_few(pad_x, pad_ids, torch.cat([wts, wts[:2]]), *w, out_dtype=torch.float32)
     assert torch.equal(padded[:T], alone) and bool((padded[T:] == 0).all())
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "bf16"])
+def test_one_expert_with_every_row(kind):
+    T, k, G, K, F, N = 1024, 1, 1, 128, 128, 128
+    w, d1, d2 = _layer(G, K, F, N, kind, False)
+    x, ids, wts = _inputs(T, k, G, K, seed=12)
+    y = gm.gmm_moe_few(x, ids, wts, *w, out_dtype=torch.float32)
+    ref, bound = _ref(x, ids, wts, d1, d2)
+    _check(y, ref, bound, kind)
+
+
+def _sparse(C, cols, kind, trans, seed):
+    """A weight [1, C, cols] whose columns have 8 entries of +-1 (an entry hit
+    twice is their sum), the entries' rows [8, cols] and signs."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    rows = torch.randint(0, C, (8, cols), generator=g, device=DEV)
+    rows[0, ::2], rows[1, 1::2] = C - 1, 0
+    sign = torch.randint(0, 2, (8, cols), generator=g, device=DEV).float() * 2 - 1
+    w = torch.zeros(C, cols, device=DEV)
+    w.index_put_((rows, torch.arange(cols, device=DEV).expand(8, -1)), sign, accumulate=True)
+    w = (w.t() if trans else w).contiguous()
+    w = w.to(torch.float8_e4m3fn).view(torch.uint8) if kind == "e4m3" else w.bfloat16()
+    return w[None], rows, sign.double()
+
+
+@pytest.mark.parametrize("K,F,N", [(1 << 20, 128, 128), (128, 1 << 19, 128), (128, 128, 1 << 20)])
+@pytest.mark.parametrize("kind,trans", [("e4m3", False), ("e4m3", True), ("bf16", False), ("bf16", True)])
+def test_largest_sizes(K, F, N, kind, trans):
+    """The longest contractions and widest rows, with weights sparse enough that
+    every entry shows: x holds integers up to 8, so gate and up are exact; h is
+    rounded to bf16 (2^-8) after 1e-5 of SwiGLU, and split for E4M3 weights to
+    2^-22 of its row's largest."""
+    w1, r1, s1 = _sparse(K, 2 * F, kind, trans, 1)
+    w2, r2, s2 = _sparse(F, N, kind, trans, 2)
+    g = torch.Generator().manual_seed(3)
+    x = torch.randint(-8, 9, (2, K), generator=g).bfloat16().to(DEV)
+    ids = torch.zeros(2, 1, dtype=torch.int32, device=DEV)
+    wts = torch.tensor([[1.0], [-0.5]], device=DEV)
+    one = lambda n: torch.ones(1, n, device=DEV) if kind == "e4m3" else None  # noqa: E731
+    y = gm.gmm_moe_few(x, ids, wts, w1, one(2 * F), w2, one(N), transpose_rhs=trans, out_dtype=torch.float32)
+    for t in range(2):
+        z = (x[t].double()[r1] * s1).sum(0)
+        h = z[:F] * torch.sigmoid(z[:F]) * z[F:]
+        terms = h[r2] * s2
+        bound = (2.0 ** -8 + 1e-5) * terms.abs().sum(0) + 8 * 2.0 ** -22 * h.abs().max()
+        assert_within(y[t], (wts[t, 0].double() * terms.sum(0)).cpu().numpy(), bound.cpu().numpy(), f"token {t}")

@@ -238,3 +238,27 @@ def test_combine_dweight_empty():
     out = gm.gmm_combine_dweight(torch.ones(2, 16, dtype=torch.bfloat16, device=DEV), rows[:0],
                                  torch.zeros(2, 2, dtype=torch.int32, device=DEV))
     assert bool((out == 0).all())
+
+
+def test_the_most_tokens():
+    T = 1 << 24
+    x = torch.randn(T, 2, generator=torch.Generator(device=DEV).manual_seed(5), device=DEV)
+    ids, w = gm.gmm_router_topk(x, 1)
+    assert torch.equal(ids[:, 0], (x[:, 1] > x[:, 0]).int())
+    p = torch.softmax(x.double(), 1)
+    # an exponential (4 ulp) over a sum of two, and a division
+    assert bool(((w.double() - p.amax(1, keepdim=True)).abs() <= 1e-6).all())
+    dl = gm.gmm_router_topk_bwd(torch.ones_like(w), x, ids)
+    ref = p[:, 0] * p[:, 1] * torch.where(ids[:, 0] == 0, 1.0, -1.0)  # d p_max / d x_0
+    assert bool(((dl[:, 0].double() - ref).abs() <= 1e-6).all()) and bool(((dl[:, 1].double() + ref).abs() <= 1e-6).all())
+
+
+def test_combine_dweight_offsets_beyond_31_bits():
+    R, N = 300_000, 8192
+    g = torch.Generator(device=DEV).manual_seed(6)
+    rows = torch.empty(R, N, dtype=torch.bfloat16, device=DEV).normal_(generator=g)
+    dy = torch.randn(2, N, generator=g, device=DEV).bfloat16()
+    slot = torch.tensor([[R - 1, 0], [R - 2, 280_000]], dtype=torch.int32, device=DEV)
+    dw = gm.gmm_combine_dweight(dy, rows, slot)
+    terms = dy.double()[:, None, :] * rows[slot.long()].double()
+    assert bool(((dw.double() - terms.sum(2)).abs() <= (N / 128 + 26) * 2.0 ** -24 * terms.abs().sum(2)).all())
