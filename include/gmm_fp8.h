@@ -264,8 +264,9 @@ gmm_status gmm_fwd_act(gmm_operand lhs, gmm_operand rhs, int transpose_rhs, cons
 
 /*
  * Gradient of that epilogue.  dout: bf16 [M, Nout]; preact: bf16 [M, N], the
- * kept z.  dz: bf16 [M, N] = dout * act'(z) (SwiGLU: d gate | d up), the dout
- * of gmm_dlhs, tgmm_drhs and gmm_backward; it may be the preact buffer itself
+ * kept z.  dz: bf16 [M, N] = dout * act'(z) (SwiGLU: d gate | d up; ReLU: dout
+ * where z > 0, else 0 whatever dout is), the dout of gmm_dlhs, tgmm_drhs and
+ * gmm_backward; it may be the preact buffer itself
  * (never dout's: SwiGLU writes twice dout's columns).  dbias: device float
  * [G, N] or NULL: sum of dz over the group's rows in fp32, before dz is
  * rounded; the order of the sum depends on the sizes only.  Empty groups get

@@ -86,12 +86,11 @@ __device__ __forceinline__ float2 act2(float2 z) {
   }
 }
 
-// d act(z) / dz
+// d act(z) / dz (ReLU's gradient chooses and has no slope here)
 template <int kAct>
 __device__ __forceinline__ float2 slope2(float2 z) {
-  if constexpr (kAct == GMM_ACT_RELU) {
-    return make_float2(z.x > 0.0f ? 1.0f : 0.0f, z.y > 0.0f ? 1.0f : 0.0f);
-  } else if constexpr (kAct == GMM_ACT_SILU) {
+  static_assert(kAct != GMM_ACT_RELU && kAct != GMM_ACT_SWIGLU);
+  if constexpr (kAct == GMM_ACT_SILU) {
     const float2 s = sigmoid2(z);
     return __ffma2_rn(__fmul2_rn(z, s), __ffma2_rn(s, splat(-1.0f), splat(1.0f)), s);
   } else if constexpr (kAct == GMM_ACT_GELU) {

@@ -121,6 +121,9 @@ __global__ void __launch_bounds__(kActThreads, 4) act_bwd_kernel(const ActBwdPar
             const float2 ds = __ffma2_rn(as, __ffma2_rn(s, splat(-1.0f), splat(1.0f)), s);
             o[0][i] = __fmul2_rn(__fmul2_rn(d, b), ds);
             o[kParts - 1][i] = __fmul2_rn(d, as);
+          } else if constexpr (kAct == GMM_ACT_RELU) {
+            // a choice, not a product: an infinite or NaN d times 0 is NaN
+            o[0][i] = make_float2(a.x > 0.0f ? d.x : 0.0f, a.y > 0.0f ? d.y : 0.0f);
           } else {
             o[0][i] = __fmul2_rn(d, slope2<kAct>(a));
           }
