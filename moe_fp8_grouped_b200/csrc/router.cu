@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kRouterWarps * 32) router_topk_bwd_kernel(cons
     const float pr = valid ? fast_exp(xs - m) / s : 0.0f;
     c = pr * dw;
     const float dot = warp_sum(valid ? c : 0.0f);
-    const float f = s > 0.0f ? dot / s : 0.0f;
+    const float f = s == 0.0f ? 0.0f : dot / s;  // s = 0: every expert is masked; a NaN in the row stays
     for (int e2 = lane; e2 < E; e2 += 32) row[e2] = -row[e2] * f;
   }
   __syncwarp();
