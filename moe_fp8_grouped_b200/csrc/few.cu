@@ -180,6 +180,7 @@ struct FewTail {
   int last[kSt];       // the stage's newest copy (unit), -1: none
   uint32_t tmem_slot;
   int abort_flag, no_abort;
+  uint32_t gave_up;  // GMM_DEV_TIMEOUT of a wait of this CTA
   Product prod[2];
   int scan[kFewThreads / 32];        // rows and groups of each warp's experts
   uint32_t big[kFewOwnTokens];       // largest magnitude of each token's row (bf16 bits)
@@ -279,6 +280,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   if (tid == 0) {
     t.abort_flag = 0;
     t.no_abort = 0;
+    t.gave_up = 0;
     if (blockIdx.x == 0) *p.status = 0;
   }
   fence_barrier_init();
@@ -394,9 +396,12 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     __syncthreads();
   }
 
-  const WaitCtl ctl{p.wait_limit_ns, &t.abort_flag, p.status};
+  // A wait that gives up is kept in shared memory and reported when the CTA
+  // leaves: no grid barrier lies between CTA 0's reset of the status word and
+  // the first waits, so a report from here could be reset again.
+  const WaitCtl ctl{p.wait_limit_ns, &t.abort_flag, &t.gave_up};
   // a CTA leaves only when its own copies and MMAs have landed, however short the caller's limit
-  const WaitCtl ctl_drain{max(p.wait_limit_ns, static_cast<uint64_t>(1000000000)), &t.no_abort, p.status};
+  const WaitCtl ctl_drain{max(p.wait_limit_ns, static_cast<uint64_t>(1000000000)), &t.no_abort, &t.gave_up};
   const Product prod1 = t.prod[0], prod2 = t.prod[1];
   const int n1 = prod1.n, n2 = prod2.n;
   // E4M3 weights use hi and lo columns, bf16 one column a row
@@ -790,6 +795,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       if (t.last[s] >= 0) mbar_wait(&t.full_a[s], (t.last[s] / kSt) & 1, ctl_drain);
   tc_fence_before();
   __syncthreads();
+  if (tid == 0 && t.gave_up) atomicOr(p.status, t.gave_up);  // after the reset: the products' grid barriers lie between
   if (warp == kMmaWarp0) {
     tc_fence_after();
     tmem_dealloc(tbase, kTmem);

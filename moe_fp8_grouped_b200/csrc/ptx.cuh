@@ -51,17 +51,18 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
 }
 
 // State shared by the waits of one CTA: a time limit, the CTA's abort flag in
-// shared memory and the call's status word in global memory.
+// shared memory and the word that takes GMM_DEV_TIMEOUT: the call's status word
+// in global memory, or one in shared memory that the CTA passes on later.
 struct WaitCtl {
   uint64_t limit_ns;
   volatile int *abort_flag;  // shared memory
-  uint32_t *status;          // global memory
+  uint32_t *status;
 };
 
 // Waits until the phase with the given parity of `bar` has completed.  Gives
 // up (returns false) when another role of the CTA has aborted, or after
 // `limit_ns`, in which case it raises the CTA's abort flag and records
-// GMM_DEV_TIMEOUT in the status word.  Never traps.
+// GMM_DEV_TIMEOUT in `status`.  Never traps.
 __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, const WaitCtl &ctl) {
   const uint32_t b = smem_u32(bar);
   if (mbar_try_wait(b, parity)) return true;
