@@ -316,7 +316,8 @@ gmm_status gmm_moe_few(const void *x_bf16, const int32_t *expert_ids, const floa
  * compare as exact numbers: fp32 near-ties are decided in fp64); a NaN key
  * counts as the largest.  An expert whose logit or key is -inf is never
  * chosen: a token with fewer than k others gets id -1 and weight 0 for the
- * rest (gmm_moe_few and gmm_combine_rows skip such ids and slots).
+ * rest (gmm_moe_few, gmm_router_topk_bwd and the expert-parallel layer in
+ * moe_fp8_grouped_b200/ep.py skip such ids, gmm_combine_rows such slots).
  *   weights[t, j] = scale * p_j, or with normalize scale * p_j / (sum of the
  *   chosen p), which is finite even where every chosen p underflows.
  * expert_ids: device int32 [T, k]; weights: device float [T, k].

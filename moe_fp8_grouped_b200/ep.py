@@ -32,6 +32,8 @@ import torch.distributed as dist
 from . import _binding as B
 from .ops import _check, _dev, _stream, gmm_backward, gmm_fwd
 
+_NONE = 2 ** 31 - 1  # sort key of a choice without an expert (id -1 without its sign bit)
+
 
 @dataclass
 class Route:
@@ -44,10 +46,14 @@ class Route:
     counts: torch.Tensor        # int64 [E]: rows per expert from this rank
     send_splits: list | None    # rows sent to each rank (host ints; None until synchronized)
     bad: torch.Tensor | None = None   # int64 [1] on the device: expert ids out of range
+    missing: torch.Tensor | None = None  # bool [T*k]: choices without an expert (id -1)
 
 
 def route(expert_ids: torch.Tensor, E: int, P: int, validate: bool = True, sync: bool = True) -> Route:
     """Sort this rank's routed rows by expert: the send order of the exchange.
+    An id of -1 is a choice without an expert (gmm_router_topk gives it where
+    fewer than k are left): it comes last in the order, behind the experts'
+    rows, and counts for no expert.
 
     sync=True (the default): one host synchronization reads the range check of
     the ids and, with more than one rank, the send splits.  sync=False: nothing
@@ -55,24 +61,37 @@ def route(expert_ids: torch.Tensor, E: int, P: int, validate: bool = True, sync:
     None (``exchange_counts`` then reads both with the arrival counts, in the
     exchange's one synchronization).  validate=False (one rank only) skips the
     check, for ids already checked (for example in a captured CUDA graph);
-    out-of-range ids are then counted against the nearest valid expert."""
+    ids from E on are then counted against the last expert, and send_splits
+    counts all T*k choices."""
     if E % P:
         raise ValueError(f"{E} experts do not split over {P} ranks")
     T, k = expert_ids.shape
-    flat = expert_ids.reshape(-1).to(torch.int64)
-    bad = ((flat < 0) | (flat >= E)).sum().view(1)
-    order = torch.argsort(flat.to(torch.int32), stable=True)  # 32-bit keys: half the radix passes
+    flat = expert_ids.reshape(-1)
+    if flat.dtype != torch.int32:
+        flat = flat.clamp(-2, _NONE).to(torch.int32)  # out of range stays out of range
+    key = flat & _NONE  # 32-bit keys: half the radix passes of the sort; -1 becomes the largest
+    order = torch.argsort(key, stable=True)
+    missing = flat == -1
     counts = torch.zeros(E, dtype=torch.int64, device=flat.device)
-    counts.index_add_(0, flat.clamp(0, E - 1), torch.ones_like(flat))
-    send = counts.view(P, E // P).sum(dim=1)
+    counts.index_add_(0, key.clamp(max=E - 1), (~missing).to(torch.int64))
     if P == 1 and not validate:
-        return Route(E, P, k, order, counts, [T * k])
+        return Route(E, P, k, order, counts, [T * k], None, missing)
+    bad = (flat.clamp(-1, E - 1) != flat).sum().view(1)
     if not sync:
-        return Route(E, P, k, order, counts, None, bad)
-    host = torch.cat([bad, send]).tolist() if P > 1 else bad.tolist()
-    if host[0]:
+        return Route(E, P, k, order, counts, None, bad, missing)
+    host = torch.cat([counts, bad]).tolist()
+    if host[E]:
         raise ValueError("expert id out of range")
-    return Route(E, P, k, order, counts, host[1:] if P > 1 else [T * k])
+    return Route(E, P, k, order, counts, [sum(host[r:r + E // P]) for r in range(0, E, E // P)], None, missing)
+
+
+def _slots(rt: Route) -> torch.Tensor:
+    """[T, k] int32: which of the rows that came back (in the order they were
+    sent) belongs to each choice, -1 for a choice without an expert."""
+    n, dev = rt.order.numel(), rt.order.device
+    slot = torch.empty(n, dtype=torch.int32, device=dev)
+    slot.scatter_(0, rt.order, torch.arange(n, dtype=torch.int32, device=dev)).masked_fill_(rt.missing, -1)
+    return slot.view(-1, rt.k)
 
 
 def exchange_counts(rt: Route, group=None):
@@ -199,14 +218,17 @@ def ep_moe_fwd(x_codes: torch.Tensor, static_scale: torch.Tensor, expert_ids: to
     """One expert-parallel expert projection for this rank's T tokens.
 
     x_codes: E4M3 codes [T, K] of the tokens (static rule, ``static_scale``
-    one float on the device); expert_ids / weights: [T, k] routing; w_codes /
-    w_scales: this rank's experts [E/P, K, N] and [E/P, N].  Returns
+    one float on the device); expert_ids / weights: [T, k] routing (an id of
+    -1, as gmm_router_topk gives where fewer than k experts are left,
+    contributes nothing); w_codes / w_scales: this rank's experts [E/P, K, N]
+    and [E/P, N].  Returns
     y [T, N] = sum_j weights[t, j] * (x[t] @ W[expert_ids[t, j]]).
     On one rank with validate=False nothing synchronizes with the host, so
     the call can be captured in a CUDA graph (see EPForwardGraph).
-    keep_rows=True returns (y, h, slot): the experts' output rows h [T*k, N] as
-    they came back and slot [T, k] (int32), the row of each choice, from which
-    gmm_combine_dweight(dy, h, slot) gives the routing weights' gradient.
+    keep_rows=True returns (y, h, slot): the experts' output rows h as they
+    came back ([T*k, N]; over several ranks without the choices of id -1) and
+    slot [T, k] (int32), the row of each choice (-1 for an id of -1), from
+    which gmm_combine_dweight(dy, h, slot) gives the routing weights' gradient.
     """
     P = dist.get_world_size(group) if dist.is_initialized() else 1
     El, K, N = w_codes.shape
@@ -219,10 +241,11 @@ def ep_moe_fwd(x_codes: torch.Tensor, static_scale: torch.Tensor, expert_ids: to
     send = gather_rows(x_codes, order // k)
     if P == 1:
         # nothing to exchange: the sorted rows are already grouped by expert
+        # (rows of missing choices lie behind the last group)
         back_rows, gsz = send, rt.counts
     else:
         recv_counts, arrive = exchange_counts(rt, group)
-        recv = exchange_rows(send, rt.send_splits, arrive, group)
+        recv = exchange_rows(send[:sum(rt.send_splits)], rt.send_splits, arrive, group)
         perm, inv, gsz = local_order(recv_counts, sum(arrive))
         back_rows = gather_rows(recv, perm)
     if back_rows.shape[0]:
@@ -233,9 +256,7 @@ def ep_moe_fwd(x_codes: torch.Tensor, static_scale: torch.Tensor, expert_ids: to
     if P > 1:
         # back in arrival order, then to the source ranks
         h = exchange_rows(gather_rows(h, inv), arrive, rt.send_splits, group)
-    # h[i] is the result of flat position order[i]; slot of (t, j) = i
-    slot = torch.empty_like(order).scatter_(0, order, torch.arange(order.numel(), device=order.device))
-    slot = slot.view(T, k).to(torch.int32)
+    slot = _slots(rt)  # h[i] is the result of flat position order[i]
     y = combine_rows(h, slot, weights, out_dtype)
     return (y, h, slot) if keep_rows else y
 
@@ -294,8 +315,9 @@ def ep_moe_bwd(x_codes: torch.Tensor, static_scale: torch.Tensor, expert_ids: to
     else:
         recv_counts, arrive = exchange_counts(rt, group)  # the one host synchronization
         perm, inv, gsz = local_order(recv_counts, sum(arrive))
-        xr = gather_rows(exchange_rows(send_x, rt.send_splits, arrive, group), perm)
-        dr = gather_rows(exchange_rows(send_d, rt.send_splits, arrive, group), perm)
+        n = sum(rt.send_splits)
+        xr = gather_rows(exchange_rows(send_x[:n], rt.send_splits, arrive, group), perm)
+        dr = gather_rows(exchange_rows(send_d[:n], rt.send_splits, arrive, group), perm)
     dw = torch.empty((El, K, N), dtype=dw_dtype, device=x_codes.device)
     if xr.shape[0]:
         dl, dw = gmm_backward(xr, dr, w_codes, w_scales, gsz.to(torch.int32), rule="static",
@@ -305,6 +327,5 @@ def ep_moe_bwd(x_codes: torch.Tensor, static_scale: torch.Tensor, expert_ids: to
         dw.zero_()
     if P > 1:
         dl = exchange_rows(gather_rows(dl, inv), arrive, rt.send_splits, group)
-    slot = torch.empty_like(order).scatter_(0, order, torch.arange(order.numel(), device=order.device))
     ones = torch.ones((T, k), dtype=torch.float32, device=x_codes.device)
-    return combine_rows(dl, slot.view(T, k), ones, dx_dtype), dw
+    return combine_rows(dl, _slots(rt), ones, dx_dtype), dw
