@@ -219,12 +219,12 @@ __device__ __forceinline__ void epi_products(const float2 *acc, const float *cf,
   }
 }
 
-// A thread's kCh * 32 tile columns (column half h of column tile ct; for
+// A thread's 128 tile columns (column half h of the 256-column tile ct; for
 // SwiGLU 64 gate columns, then the matching 64 up columns); cf: the tile's
 // column scales in shared memory (scaled: there are any).
-template <int kCh, int kEpi, bool kBefore, bool kAfter>
+template <int kEpi, bool kBefore, bool kAfter>
 __device__ __forceinline__ void epi_tile(const GemmParams &p, int g, int64_t row, int ct, int h,
-                                         const float2 (&acc)[kCh * 16], const float *cf, bool scaled, float before,
+                                         const float2 (&acc)[64], const float *cf, bool scaled, float before,
                                          float after, bool out_v8) {
   float2 o[16], u[16];
   if constexpr (kEpi == GMM_ACT_SWIGLU) {
@@ -232,13 +232,13 @@ __device__ __forceinline__ void epi_tile(const GemmParams &p, int g, int64_t row
     for (int c = 0; c < 2; ++c) {
       const int in_tile = h * 64 + c * 32;
       epi_products<kBefore, kAfter>(acc + c * 16, cf + in_tile, scaled, before, after, o);
-      epi_products<kBefore, kAfter>(acc + (32 + c * 16) % (kCh * 16), cf + 128 + in_tile, scaled, before, after, u);
+      epi_products<kBefore, kAfter>(acc + 32 + c * 16, cf + 128 + in_tile, scaled, before, after, u);
       epi_finish<kEpi>(p, g, row, true, ct * 128 + in_tile, o, u, out_v8);
     }
   } else {
 #pragma unroll
-    for (int c = 0; c < kCh; ++c) {
-      const int in_tile = h * kCh * 32 + c * 32, col = ct * kCh * 64 + in_tile;
+    for (int c = 0; c < 4; ++c) {
+      const int in_tile = h * 128 + c * 32, col = ct * 256 + in_tile;
       if (col >= p.ncols) continue;
       epi_products<kBefore, kAfter>(acc + c * 16, cf + in_tile, scaled, before, after, o);
       epi_finish<kEpi>(p, g, row, false, col, o, u, out_v8);

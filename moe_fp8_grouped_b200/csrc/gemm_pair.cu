@@ -185,6 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kBKe = 128 / kElem;                 // contraction elements per stage
   constexpr int kMmaK = 32 / kElem;                 // contraction elements per MMA
   static_assert(kTN == 256 || (kTN == 128 && kPair && kPromote && !kBMN), "128-column tiles: pairs, promoted, K-major B");
+  static_assert(!kPromote || kEpi == kNoEpi, "promoted products with a fused epilogue take one-CTA tiles");
   constexpr int kBS = (kTN * 128) / kCta;           // bytes of B per CTA per stage
   constexpr int kBBoxes = kBMN ? (2 / kCta) * kElem : 1;  // TMA boxes per B stage (128-byte wide if MN-major)
   constexpr int kBBoxBytes = kBS / kBBoxes;
@@ -615,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         row_ok = true;
       }
       if constexpr (kEpi != kNoEpi) {
-        if (row_ok) epi_prefetch(p, orow, sw ? t.ct * 128 + h * 64 : col0, sw ? 64 : kTN / 2);
+        if (row_ok) epi_prefetch(p, orow, sw ? t.ct * 128 + h * 64 : col0, sw ? 64 : 128);
       }
       // writes 32 tile columns starting at tile column col (a multiple of 32)
       auto emit = [&](int col, const float(&o)[32]) {
@@ -717,12 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (b + 1 < t.nblocks) release_slot(slot);  // the last slot is read again below
         }
         if (!ok) break;
-        if constexpr (kEpi != kNoEpi) {
-          if (row_ok)
-            epi_tile<kCh, kEpi, false, kBlkScales>(p, t.g, orow, t.ct, h, acc, s_scol + slot * kBN,
-                                                 p.col_scale != nullptr, 1.0f, p.static_scale ? s_eff : 1.0f,
-                                                 out_v8);
-        } else if (row_ok) {
+        if (row_ok) {
           // per-channel rhs column scale (in every unit's slot); static lhs: s
           const float fin = ((kTg || kBlkScales) && p.static_scale) ? s_eff : 1.0f;
           const bool colmul = !kTg && p.col_scale != nullptr;
@@ -817,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (two) ++n1;
         if constexpr (kEpi != kNoEpi) {
           if (row_ok)
-            epi_tile<4, kEpi, true, false>(p, t.g, orow, t.ct, h, acc, s_scol + slot * kBN, need_col,
+            epi_tile<kEpi, true, false>(p, t.g, orow, t.ct, h, acc, s_scol + slot * kBN, need_col,
                                            p.static_scale ? s_eff : 1.0f, 1.0f, out_v8);
         } else if (row_ok) {
           const float s0 = p.static_scale ? s_eff : 1.0f;

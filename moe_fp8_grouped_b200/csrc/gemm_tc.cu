@@ -673,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         if constexpr (kEpi != kNoEpi) {
           if (row_ok)
-            epi_tile<4, kEpi, false, kBlkScales>(p, t.g, orow, t.ct, h, acc, s_scol + slot * kBN,
+            epi_tile<kEpi, false, kBlkScales>(p, t.g, orow, t.ct, h, acc, s_scol + slot * kBN,
                                                  p.col_scale != nullptr, 1.0f, p.static_scale ? s_eff : 1.0f,
                                                  out_v8);
         } else if (row_ok) {
@@ -777,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (two) ++n1;
         if constexpr (kEpi != kNoEpi) {
           if (row_ok)
-            epi_tile<4, kEpi, true, false>(p, t.g, orow, t.ct, h, acc, s_scol + slot * kBN, need_col,
+            epi_tile<kEpi, true, false>(p, t.g, orow, t.ct, h, acc, s_scol + slot * kBN, need_col,
                                            p.static_scale ? s_eff : 1.0f, 1.0f, out_v8);
         } else if (row_ok) {
           const float s0 = p.static_scale ? s_eff : 1.0f;
