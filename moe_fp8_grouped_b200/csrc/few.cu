@@ -65,10 +65,17 @@ namespace {
 
 constexpr int kFewThreads = 512;
 constexpr int kFewMaxSlices = 16;
-// Tokens whose largest magnitudes every CTA finds on its own; more are shared
-// through memory and one more barrier (2 us; 16 tokens of 7168 values took the
-// same 625 to 627 us either way, four tokens 120.1 on their own, 121.5 shared).
-constexpr int kFewOwnTokens = 30;
+// The tokens' largest magnitudes: every CTA finds all of them on its own, 15
+// warps taking pieces of 1024 values, or each row is one warp's of the grid and
+// the results are shared through memory and one more barrier.  On its own a warp
+// reads T pieces / 15 and shared it reads one row's pieces; sharing costs the
+// barrier, about two pieces: shared where (T - 15) pieces > 30.  Measured, own
+// against shared (us): K = 7168 (7 pieces), F = 2048, two of 32 experts, 2 tokens
+// 37.2 / 39.6, 8 102.4 / 103.7, 16 152.4 / 152.2, 24 156.8 / 154.7, 64 257 / 248;
+// K = 1024, F = 256, 30 tokens 23.8 / 24.2, 48 30.3 / 30.3, 64 31.4 / 31.1, 128
+// 40.1 / 38.5.
+constexpr int kFewOwnWarps = 15, kFewSharePieces = 30;
+constexpr int kFewOwnTokens = kFewOwnWarps + kFewSharePieces;  // rows of one piece; longer ones fewer
 constexpr int kUnitBytes = 16384;  // 128 columns x 128 bytes of contraction
 constexpr int kProdWarps = 2;      // warps 0-1
 constexpr int kMmaWarp0 = 2, kMmaWarps = 2;
@@ -298,7 +305,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   const uint32_t tbase = t.tmem_slot;
   // largest magnitude of each token's row: in every CTA for a few tokens, shared
   // through memory and one more barrier for more
-  const bool share = kElem == 1 && p.T > kFewOwnTokens;
+  const int pieces = (p.kb1 * 128 + 1023) >> 10;  // of a row (E4M3: kb1 blocks of 128)
+  const bool share = kElem == 1 && (p.T - kFewOwnWarps) * pieces > kFewSharePieces;
   if (warp == 0) {
     // rank of every pair within its expert, in pair order
     for (int base = 0; base < p.pairs; base += 32) {
@@ -315,8 +323,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     }
   } else if (kElem == 1) {
     // one warp per piece of 1024 values of a token's row (shared: per row)
-    const int pieces = (p.kb1 * 128 + 1023) >> 10, span = share ? pieces : 1;
-    const int w0 = share ? blockIdx.x * 15 + warp - 1 : warp - 1, step = share ? gridDim.x * 15 : 15;
+    const int span = share ? pieces : 1;
+    const int w0 = share ? blockIdx.x * kFewOwnWarps + warp - 1 : warp - 1;
+    const int step = share ? gridDim.x * kFewOwnWarps : kFewOwnWarps;
     for (int i = w0; i < (share ? p.T : p.T * pieces); i += step) {
       const int tok = share ? i : few_div(i, pieces), first = share ? 0 : i - tok * pieces;
       const __nv_bfloat16 *row = p.x + static_cast<int64_t>(tok) * (p.kb1 * 128);

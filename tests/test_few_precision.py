@@ -91,3 +91,30 @@ def test_activations_are_used_in_full(trans):
                          codes(w2), torch.ones(G, N, device=dev), transpose_rhs=trans, out_dtype=torch.float32)
     err = (got.double().cpu() - y).abs()
     assert bool((err <= bound).all()), f"{int((err > bound).sum())} outside, worst {float((err - bound).max())}"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tokens,width", [(45, 1024), (46, 1024), (30, 1152), (31, 1152), (15, 65664), (16, 65664)])
+def test_row_maxima_on_either_side_of_the_rule(tokens, width):
+    """The largest magnitude of a row, found by every CTA or shared: rows whose
+    only value other than 0 lies at a different place each, the last one too,
+    and of different sizes.  Gate and up are that value, h its SwiGLU rounded to
+    bf16 (one step where fp32 crosses a boundary), y that h."""
+    import moe_fp8_grouped_b200 as gm
+    dev = "cuda:0"
+    x = torch.zeros(tokens, width)
+    at = torch.arange(tokens) * 997 % width
+    at[0] = width - 1
+    v = (1 + torch.arange(tokens) % 128 / 128.0) * 2.0 ** (torch.arange(tokens) % 5 - 1)
+    x[torch.arange(tokens), at] = v
+    one = 0x38  # E4M3 code of 1
+    w1 = torch.full((1, width, 256), one, dtype=torch.uint8, device=dev)
+    w2 = torch.zeros(1, 128, 128, dtype=torch.uint8, device=dev)
+    w2[:, 7] = one
+    y = gm.gmm_moe_few(x.bfloat16().to(dev), torch.zeros(tokens, 1, dtype=torch.int32, device=dev),
+                       torch.ones(tokens, 1, device=dev), w1, torch.ones(1, 256, device=dev), w2,
+                       torch.ones(1, 128, device=dev), out_dtype=torch.float32)
+    h = v.double() * torch.sigmoid(v.double()) * v.double()
+    lo, hi = (h * (1 - 1e-5)).bfloat16().double(), (h * (1 + 1e-5)).bfloat16().double()
+    got = y.double().cpu()
+    assert bool(((got == lo[:, None]) | (got == hi[:, None])).all())
