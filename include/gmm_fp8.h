@@ -296,8 +296,8 @@ gmm_status gmm_act_bwd(const void *dout_bf16, const void *preact_bf16, gmm_act a
  * K, F, N multiples of 128, F <= 2^19, T * k <= 1024 (T == 0 is a no-op),
  * G <= 1024.  Every active expert's weights are read once per 32 of its rows:
  * for large T use gmm_fwd_swiglu, gmm_fwd and gmm_combine_rows.  With E4M3
- * weights a row's values below 2^-13 of its largest keep an absolute error of
- * 2^-22 of that largest.  The kernel is a cooperative launch on every SM of
+ * weights a row's values below 2^-13 of its largest have an absolute error of
+ * at most 2^-21 of that largest.  The kernel is a cooperative launch on every SM of
  * the device.  Workspace: gmm_moe_few_workspace_bytes (0 for invalid sizes),
  * read and written within the call; calls that may overlap need workspaces of
  * their own.

@@ -27,7 +27,7 @@
 // value has 8 significant bits, so scaled by a power of two (one per row, that
 // puts the row's largest magnitude into [128, 256)) it is hi + lo / 16 with two
 // E4M3 values of 4 significant bits each, exactly for values down to 2^-13 of
-// the row's largest and within 2^-22 of that largest below.  hi and lo are
+// the row's largest and within 2^-21 of that largest below.  hi and lo are
 // separate MMA columns, joined and unscaled once per tile.  (A scale per block
 // of 128 instead would need every block's accumulator read and scaled on its
 // own: that epilogue took 500 to 1000 cycles a unit and was the bound.)  bf16

@@ -17,7 +17,7 @@ struct FewParams {
   const float *weights;    // [T, k]
   const float *s1, *s2;    // [G, 2F], [G, N] (E4M3 weights)
   __nv_bfloat16 *h;        // [pairs, F] silu(gate) * up
-  uint32_t *largest;       // [T] and [pairs]: largest magnitudes of the rows of x and h (fp32 bits)
+  uint32_t *largest;       // [T] and [pairs]: largest magnitudes of the rows of x and h (bf16 bits)
   float *partial;          // [pairs][columns] sums of a product (its tiles' first slice)
   float *extra;            // few_extra_floats: the other slices of tiles left over
   void *y;                 // [T, N]
