@@ -14,9 +14,10 @@
 //
 // Phi from its tail: Phi(-a) = exp(-a^2 / 2) t Q(t), t = 1 / (1 + 0.305 a),
 // a >= 0, with Q of degree 7 fitted here (weighted least squares with
-// re-weighting towards the largest relative error, a in [0, 14]); the relative
-// error in fp32 is below 4.2e-7 for every a, so far tails keep their precision
-// and exp(-a^2 / 2) is shared with phi.
+// re-weighting towards the largest relative error, a in [0, 14]).  The relative
+// error of t Q(t) in fp32 is below 4.2e-7 for every a; that of the tail grows
+// with the rounded exponent, by about 2^-23 * a^2 / 2 (1.4e-6 up to a = 5,
+// 7.7e-6 up to 13).  exp(-a^2 / 2) is shared with phi.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -43,7 +44,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kTanhC0 = 1.5957691216057308f;              // 2 sqrt(2 / pi)
 constexpr float kTanhC1 = 1.5957691216057308f * 0.044715f;
 
-// 1 / (1 + exp(-x)): 0 and 1 far out (2^x overflows to inf, 1 / inf is 0)
+// 1 / (1 + exp(-x)): 0 and 1 far out (2^x overflows to inf, 1 / inf is 0; what
+// would be below 2^-126 is 0 too)
 __device__ __forceinline__ float2 sigmoid2(float2 x) {
   const float2 e = __fmul2_rn(x, splat(-kLog2e));
   const float2 d = __fadd2_rn(make_float2(fast_exp2(e.x), fast_exp2(e.y)), splat(1.0f));
