@@ -39,7 +39,8 @@
  *    largest finite 448).  Quantization: inv = fl32(1/s) (0 where s = 0),
  *    code = E4M3 round-to-nearest-even of fl32(x * inv) saturated to +-448.
  *    A dynamic scale is fl32(amax / 448) over a block of 128 values along the
- *    contraction axis; a scale whose inverse overflows counts as 0.
+ *    contraction axis (in gmm_fwd_act fl32(amax * fl32(1/448)), see there); a
+ *    scale whose inverse overflows counts as 0.
  *  - Shapes: K and N multiples of 128, all sizes positive, G <= 1024;
  *    M <= 2^24 with ceil(M / 128) + G <= 65535, K and N <= 2^20 (larger
  *    requests return GMM_ERR_UNSUPPORTED).
@@ -294,8 +295,12 @@ gmm_status gmm_act_bwd(const void *dout_bf16, const void *preact_bf16, gmm_act a
  * y: [T, N] of y_dtype (BF16 or F32).  With E4M3 weights a token with a value
  * that is not finite (or whose h overflows bf16) gets NaN.
  * K, F, N multiples of 128, F <= 2^19, T * k <= 1024 (T == 0 is a no-op),
- * G <= 1024.  Every active expert's weights are read once per 32 of its rows:
- * for large T use gmm_fwd_swiglu, gmm_fwd and gmm_combine_rows.  With E4M3
+ * G <= 1024.  Every active expert's weights are read once per 32 of its rows.
+ * With about eight rows an expert and more, gmm_fwd_swiglu, gmm_fwd and
+ * gmm_combine_rows (dynamic rule) are as fast or faster; measured, this call
+ * against those with their routing in a captured graph: K = 4096, F = 14336, two
+ * of 8 experts, 16 tokens 242 / 326 us, 32 308 / 328, 64 442 / 330; K = 7168,
+ * F = 2048, eight of 256, 64 tokens 1488 / 1711, 128 1922 / 1904.  With E4M3
  * weights a row's values below 2^-13 of its largest have an absolute error of
  * at most 2^-21 of that largest.  The kernel is a cooperative launch on every SM of
  * the device.  Workspace: gmm_moe_few_workspace_bytes (0 for invalid sizes),

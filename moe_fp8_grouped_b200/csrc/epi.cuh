@@ -9,10 +9,12 @@
 // before it is finished 5 to 10 %.  The bf16 family reads its chunks from TMEM
 // in one rolled loop.  The activations' instructions are what an epilogue is
 // made of: with the exact library forms of act.cuh's functions the Mixtral-like
-// up projection took 2.4 ms with SiLU and 5.1 ms with GELU, with these 1.55 and
-// 1.57 ms (1.48 ms without an epilogue).  32 accumulator columns a TMEM load and
-// 232 registers a thread instead of 216 or 224 brought them there from 1.64 and
-// 1.66 ms, and SwiGLU with a bias and kept z from 1.71 to 1.58 ms.
+// up projection (16384 x 4096 x 28672, short runs at full clocks) took 2.4 ms with
+// SiLU and 5.1 ms with GELU, with these 1.55 and 1.57 ms (1.48 ms without an
+// epilogue).  32 accumulator columns a TMEM load and 232 registers a thread
+// instead of 216 or 224 brought them there from 1.64 and 1.66 ms, and SwiGLU with
+// a bias and kept z from 1.71 to 1.58 ms.  Pass after pass, under the power cap,
+// that product takes 1.90 to 1.95 ms and the plain one 1.68.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -38,10 +38,10 @@
 // grid barrier, down product, grid barrier, weighted sum.  The producer starts
 // the down product's first copies before the barriers, so HBM keeps working
 // across them.  Measured (us): one token, two of 8 experts, K = 4096, F = 14336
-// E4M3: 70, of which 53.7 is the weights at the copy rate; 16 tokens, 8 of 256
-// experts each, K = 7168, F = 2048: 645 to 675 (684 for the expected experts);
-// the smallest layers 16 (set-up 2.4, a barrier 1.2, two chains of load,
-// multiply and sum).
+// E4M3: 70 to 74, of which 53.7 is the weights at the copy rate; 16 tokens, 8 of
+// 256 experts each, K = 7168, F = 2048: 645 to 705 from box to box (684 for the
+// expected experts at the copy rate); the smallest layers 16 (set-up 2.4, a
+// barrier 1.2, two chains of load, multiply and sum).
 //
 // Warps (512 threads, one CTA per SM): 0-1 TMA producers, 2-3 MMA issuers (2
 // owns the TMEM), 4-11 activation loaders, 12-15 epilogue (TMEM lanes 32 (w %
